@@ -433,6 +433,187 @@ wkv7_status_t wkv7_gdn_map(const wkv7_desc_t* desc, const wkv7_gdn_t* gd, const 
 wkv7_status_t wkv7_state_compose(const wkv7_desc_t* desc, const float* S, const float* P, const float* U,
                                  float* out, int transpose_p, void* stream);
 
+/*
+ * ------------------------------------------------------------------ state-space layer
+ * The other linear recurrence of language models beside WKV-7 and the gated
+ * delta rule (the pages have no passage on it): the selective state space
+ * scan with one decay per head, and what stands around it in a layer -- the
+ * short causal convolution in front (which gated-DeltaNet layers have in
+ * front of their q, k, v as well) and the RMS norm before the projections
+ * and, gated, after the scan.  Their descriptor is wkv7_desc_t again; flags
+ * are 0 or WKV7_FLAG_CHECK_FINITE (the same scan of the floating outputs).
+ * Errors as for wkv7_forward; algo is ignored except by wkv7_ssm_forward and
+ * wkv7_ssm_backward.  Sums, states, decays and statistics are fp32 (running
+ * sums of log decays fp64).  Parameter gradients are summed in a fixed order:
+ * repeated calls give the same bits.
+ *
+ * Token strides: an input whose struct has a `*_ld` field may be a slice of a
+ * wider row-major tensor (the convolution's output holds x, b and c side by
+ * side).  `ld` is the distance between consecutive tokens in elements, 0
+ * means dense; rows of the batch are T * ld apart.  ld must be at least the
+ * row's size and ld * sizeof(element) a multiple of 16 (dt: any ld >= H),
+ * else WKV7_ERR_SHAPE / WKV7_ERR_ALIGN.  Outputs and gradients are dense.
+ */
+
+/*
+ * Short causal convolution, one filter per channel, with optional SiLU:
+ *   u_t[d] = bias[d] + sum_{j < W} weight[d][W-1-j] x_{t-j}[d]
+ *   y_t[d] = u / (1 + exp(-u)) if silu, else u
+ * A tap before t = 0 reads s0 (zero if NULL); a reset at token t cuts every
+ * tap that lies before t.
+ *
+ *   desc     B, T, dtype; H and N are ignored (H >= 0)
+ *   cv       D >= 0 channels, a multiple of 8; W = 2, 3 or 4 taps (else
+ *            WKV7_ERR_UNSUPPORTED); weight fp32 [D,W], bias fp32 [D] or NULL
+ *            (both 16-byte aligned)
+ *   x        in   [B,T,D] desc->dtype (token stride x_ld)
+ *   s0       in   [B,W-1,D] desc->dtype, the inputs before t = 0, oldest
+ *                 first, or NULL for zeros
+ *   reset    in   [B,T] u8 or NULL
+ *   y        out  [B,T,D]
+ *   s_out    out  [B,W-1,D] the last W-1 inputs, oldest first, zero where a
+ *                 reset cuts them off (T < W-1: shifted in from s0), or NULL;
+ *                 must not be s0 (WKV7_ERR_UNSUPPORTED)
+ */
+typedef struct {
+  int64_t D;           /* channels, a multiple of 8 */
+  int32_t W;           /* taps: 2, 3 or 4 */
+  int32_t silu;        /* non-zero: y = silu(u) */
+  const float* weight; /* [D, W]; weight[d][W-1] multiplies the current token */
+  const float* bias;   /* [D] or NULL */
+  int64_t x_ld;        /* token stride of x in elements, 0 = D */
+} wkv7_conv_t;
+
+wkv7_status_t wkv7_conv_forward(const wkv7_desc_t* desc, const wkv7_conv_t* cv, const void* x, const void* s0,
+                                const uint8_t* reset, void* y, void* s_out, void* stream);
+
+/*
+ * Reverse mode: dy [B,T,D] and dsT [B,W-1,D] (gradient of s_out, or NULL)
+ * give dx [B,T,D], ds0 [B,W-1,D] (or NULL), and dweight fp32 [D,W], dbias
+ * fp32 [D] (each may be NULL), which are written, not added to.  `scratch`
+ * holds wkv7_conv_scratch_bytes(desc, cv) bytes (required when dweight or
+ * dbias is asked for and T > 0: WKV7_ERR_WORKSPACE).
+ */
+size_t wkv7_conv_scratch_bytes(const wkv7_desc_t* desc, const wkv7_conv_t* cv);
+wkv7_status_t wkv7_conv_backward(const wkv7_desc_t* desc, const wkv7_conv_t* cv, const void* x, const void* s0,
+                                 const uint8_t* reset, const void* dy, const void* dsT, void* dx, float* dweight,
+                                 float* dbias, void* ds0, void* scratch, void* stream);
+
+/*
+ * One decode token: x [B,D] (row stride x_ld), state [B,W-1,D] shifted in place, y
+ * [B,D].  T must be 1.  active as in wkv7_step: an inactive row keeps its
+ * state bit for bit and gets y = 0.
+ */
+wkv7_status_t wkv7_conv_step(const wkv7_desc_t* desc, const wkv7_conv_t* cv, const void* x, void* state,
+                             const uint8_t* active, void* y, void* stream);
+
+/*
+ * Selective state space scan.  Per (b, h) an fp32 state S [64][N] (row = head
+ * channel, column = state channel); with group g = h / (H / G)
+ *   d_t = softplus(dt_t[h] + dt_bias[h])   (softplus == 0: dt_t[h] + dt_bias[h])
+ *   S_t = exp(d_t A[h]) S_{t-1} + d_t x_t[h] b_t[g]^T     (reset: S_{t-1} = 0)
+ *   y_t[h] = S_t c_t[g] + D[h] x_t[h]
+ *
+ *   desc     B, T, H heads, N = 64 or 128 state channels, dtype, algo: SCAN
+ *            (token order, any dtype), CHUNKED (128-token chunks on the tensor
+ *            cores; bf16 only, else WKV7_ERR_UNSUPPORTED) or AUTO (CHUNKED
+ *            for bf16, SCAN otherwise)
+ *   sp       below
+ *   x        in   [B,T,H,64] desc->dtype;  dt  in  [B,T,H];  b, c  in  [B,T,G,N]
+ *   s0       in   [B,H,64,N] fp32 or NULL for zeros
+ *   reset    in   [B,T] u8 or NULL
+ *   y        out  [B,T,H,64];  s_out  out  [B,H,64,N] fp32 or NULL
+ *   workspace out wkv7_ssm_workspace_bytes(desc, sp) bytes: the state before
+ *            every 128th token, for the backward, then scratch; or NULL
+ *            (nothing is kept, and CHUNKED cannot split a long sequence of few heads).
+ */
+typedef struct {
+  int64_t G;            /* groups: heads that share b and c are consecutive; H % G == 0 */
+  const float* A;       /* [H] decay rates (normally < 0) */
+  const float* D;       /* [H] skip weights, or NULL for none */
+  const float* dt_bias; /* [H] or NULL */
+  int32_t softplus;     /* non-zero: d = softplus(dt + dt_bias) */
+  int64_t x_ld, dt_ld, b_ld, c_ld; /* token strides in elements, 0 = dense */
+} wkv7_ssm_t;
+
+size_t wkv7_ssm_workspace_bytes(const wkv7_desc_t* desc, const wkv7_ssm_t* sp);
+wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const void* x, const void* dt,
+                               const void* b, const void* c, const float* s0, const uint8_t* reset, void* y,
+                               float* s_out, void* workspace, void* stream);
+
+/*
+ * Reverse mode, from the workspace that the forward of the same arguments
+ * wrote (the algo may differ): dy [B,T,H,64], dsT [B,H,64,N] fp32 (gradient of
+ * s_out, or NULL) give dx [B,T,H,64], ddt [B,T,H], db, dc [B,T,G,N] (desc->dtype; db and dc
+ * are summed over the group's heads), dA [H], dD [H], ddt_bias [H] fp32 (each
+ * may be NULL) and ds0 [B,H,64,N] fp32 (or NULL).  All are written, not added
+ * to.  ddt is the gradient of the dt input (before the bias and softplus).
+ * `scratch` holds wkv7_ssm_scratch_bytes(desc, sp) bytes
+ * (WKV7_ERR_WORKSPACE if it or the workspace is NULL when T > 0).
+ */
+size_t wkv7_ssm_scratch_bytes(const wkv7_desc_t* desc, const wkv7_ssm_t* sp);
+wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const void* x, const void* dt,
+                                const void* b, const void* c, const float* s0, const uint8_t* reset,
+                                const void* dy, const float* dsT, const void* workspace, void* dx, void* ddt,
+                                void* db, void* dc, float* dA, float* dD, float* ddt_bias, float* ds0,
+                                void* scratch, void* stream);
+
+/*
+ * One decode token on B*H resident states in place: x [B,H,64], dt [B,H], b,
+ * c [B,G,N], state [B,H,64,N] fp32, y [B,H,64].  T must be 1.  active as in
+ * wkv7_step.
+ */
+wkv7_status_t wkv7_ssm_step(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const void* x, const void* dt,
+                            const void* b, const void* c, float* state, const uint8_t* active, void* y,
+                            void* stream);
+
+/*
+ * RMS norm over `groups` equal slices of each of the B*T rows:
+ *   h   = x                                    (other == NULL)
+ *       = round(x + other), stored to h_out    (gate == 0: the residual's addition)
+ *       = x * silu(other)                      (gate != 0)
+ *   out = h / sqrt(mean(h^2 over the slice) + eps) * weight
+ * The norm is of the sum as it is stored (rounded to desc->dtype), which is
+ * what the backward reads.
+ *
+ *   desc     B, T, dtype (H and N ignored)
+ *   rn       D channels; D % groups == 0, D / groups a multiple of 8 and at
+ *            most 16384 (else WKV7_ERR_UNSUPPORTED); weight fp32 [D], 16-byte
+ *            aligned; eps > 0
+ *   x, other in   [B,T,D] desc->dtype (other may be NULL)
+ *   h_out    out  [B,T,D]: required with gate == 0 and `other`, else NULL; may be x or other
+ *   out      out  quant_block == 0: [B,T,D] desc->dtype.  Otherwise e4m3
+ *                 (1 byte) with `scale` fp32, value = code * scale: one scale per
+ *                 quant_block = 128 channels ([B,T,D/128]; D / groups a multiple of 128) or,
+ *                 with quant_block = -1, per slice ([B,T,groups]).  scale = max|.| / 448
+ *                 (at least 2^-100; 1 for a block of zeros).
+ */
+typedef struct {
+  int64_t D;
+  int64_t groups;
+  const float* weight;
+  float eps;
+  int32_t gate;        /* how `other` enters: 0 added, else as a gate */
+  int32_t quant_block; /* 0, 128 or -1 */
+} wkv7_rms_t;
+
+wkv7_status_t wkv7_rms_forward(const wkv7_desc_t* desc, const wkv7_rms_t* rn, const void* x, const void* other,
+                               void* h_out, void* out, float* scale, void* stream);
+
+/*
+ * Reverse mode from dout [B,T,D] (quant_block must be 0).  Without a gate x
+ * is h as stored and `other` NULL; dx is the gradient of h, which is that of
+ * both summands, and dh [B,T,D] (or NULL), the gradient that reaches h
+ * directly, is added in before rounding.  With a gate x and `other` are the
+ * forward's, dother receives the gate's gradient and dh is NULL.  dweight
+ * fp32 [D] (or NULL) is written from `scratch`, wkv7_rms_scratch_bytes(desc,
+ * rn) bytes (WKV7_ERR_WORKSPACE if missing).
+ */
+size_t wkv7_rms_scratch_bytes(const wkv7_desc_t* desc, const wkv7_rms_t* rn);
+wkv7_status_t wkv7_rms_backward(const wkv7_desc_t* desc, const wkv7_rms_t* rn, const void* x, const void* other,
+                                const void* dout, const void* dh, void* dx, void* dother, float* dweight,
+                                void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,377 @@
+// RMS norm over equal slices of each row, with the residual's addition or a SiLU gate before it and an optional
+// e4m3 output (wkv7_rms_forward / wkv7_rms_backward):
+//   h = x | round(x + other) | x silu(other),   out = h rstd weight,   rstd = 1 / sqrt(mean(h^2) + eps)
+// and, with g = dout weight and m = mean(g h rstd) over the slice,
+//   dh = rstd (g - h rstd m) [+ the gradient reaching h directly],   dweight = sum over rows of dout h rstd,
+//   gate: dx = dh silu(z), dz = dh x silu'(z).
+//
+// HBM-bound: every input is read once and every output written once.  A slice is held in the registers of TPS
+// threads (a power of two; 1, 2 or 4 16-byte vectors each), so both reductions and the outputs come from one
+// read.  Up to 32 threads reduce by shuffles alone; wider slices add one pass through shared memory.  Short
+// slices share a CTA of 256 threads.
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+#include "layer_util.cuh"
+#include "state_space.h"
+
+namespace wkv7 {
+namespace {
+
+enum Mode { kPlain = 0, kResidual = 1, kGate = 2 };
+constexpr int kCta = 256;
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100: its reciprocal and the scaled values stay finite
+
+// Maximum that keeps a NaN, so that a block that holds one gets a NaN scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / kE4m3Max), kMinScale); }
+
+// Sum over the TPS threads of a slice of two values at once.  All threads of the CTA call it together.
+struct Pair { float a, b; };
+template <bool MAXA>
+__device__ __forceinline__ Pair slice_reduce(Pair v, int tps, float (*sm)[2]) {
+  const int w = tps < 32 ? tps : 32;
+  for (int o = w / 2; o; o >>= 1) {
+    const float a = __shfl_xor_sync(0xffffffffu, v.a, o);
+    v.a = MAXA ? max_nan(v.a, a) : v.a + a;
+    v.b += __shfl_xor_sync(0xffffffffu, v.b, o);
+  }
+  if (tps <= 32) return v;
+  const int warp = threadIdx.x >> 5, nw = tps >> 5, first = warp & ~(nw - 1);
+  __syncthreads();   // the last use of `sm` is over
+  if ((threadIdx.x & 31) == 0) {
+    sm[warp][0] = v.a;
+    sm[warp][1] = v.b;
+  }
+  __syncthreads();
+  Pair r{sm[first][0], sm[first][1]};
+  for (int i = 1; i < nw; ++i) {
+    r.a = MAXA ? max_nan(r.a, sm[first + i][0]) : r.a + sm[first + i][0];
+    r.b += sm[first + i][1];
+  }
+  return r;
+}
+
+struct Shape {
+  int64_t L, slices;   // channels of a slice; rows * groups
+  int tps, spc;        // threads per slice, slices per CTA
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void store_e4m3(uint8_t* o, const float (&q)[V]) {
+  uint32_t w[V / 4];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i], q[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | (hi << 16);
+  }
+  if (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[V / 4 - 1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+}
+
+template <typename T, int VPT, int MODE, int QUANT>   // QUANT: 0 none, 1 per 128 channels, 2 per slice
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const RmsArgs p, const Shape s) {
+  constexpr int V = Vec16<T>::n;
+  using VT = VecOf<T, V>;
+  __shared__ float sm[32][2];
+  const int lane = threadIdx.x % s.tps, sub = threadIdx.x / s.tps;
+  const int64_t nv = s.L / V, total = p.rows * p.D;
+  for (int64_t s0 = int64_t(blockIdx.x) * s.spc; s0 < s.slices; s0 += int64_t(gridDim.x) * s.spc) {
+    const int64_t slice = s0 + sub;
+    const int64_t row = slice / p.groups, g = slice - row * p.groups;
+    const int64_t base = row * p.D + g * s.L;
+    typename VT::R rx[VPT], rz[VPT];
+    bool act[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = int64_t(i) * s.tps + lane;
+      act[i] = slice < s.slices && v < nv && range_ok(base + v * V, V, total, p.status);
+      if (act[i]) {
+        rx[i] = VT::load(static_cast<const T*>(p.x) + base + v * V);
+        if (MODE != kPlain) rz[i] = VT::load(static_cast<const T*>(p.other) + base + v * V);
+      }
+    }
+    float h[VPT][V];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (act[i]) {
+        VT::get(rx[i], h[i]);
+        if (MODE != kPlain) {
+          float z[V];
+          VT::get(rz[i], z);
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            // the stored sum is normalised, so that the backward, which reads it, sees the same h
+            h[i][e] = MODE == kResidual ? Elt<T>::to_f32(Elt<T>::from_f32(h[i][e] + z[e])) : h[i][e] * (z[e] * sigmoid_of<T>(z[e]));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[i][e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    }
+    const float rstd = rsqrtf(slice_reduce<false>(Pair{ss, 0.f}, s.tps, sm).a / float(s.L) + p.eps);
+    if (MODE == kResidual)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (act[i]) VT::store(static_cast<T*>(p.h_out) + base + (int64_t(i) * s.tps + lane) * V, h[i]);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = int64_t(i) * s.tps + lane;
+      if (act[i]) {
+        const float4* w = reinterpret_cast<const float4*>(p.weight + g * s.L + v * V);
+#pragma unroll
+        for (int u = 0; u < V / 4; ++u) {
+          const float4 w4 = __ldg(w + u);
+          h[i][4 * u] *= rstd * w4.x; h[i][4 * u + 1] *= rstd * w4.y;
+          h[i][4 * u + 2] *= rstd * w4.z; h[i][4 * u + 3] *= rstd * w4.w;
+        }
+        if (QUANT == 0) VT::store(static_cast<T*>(p.out) + base + v * V, h[i]);
+      }
+      if (QUANT) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = max_nan(m, fabsf(h[i][e]));
+        if (QUANT == 1) {   // 128 channels are 128 / V neighbouring threads (tps >= that many)
+#pragma unroll
+          for (int o = 64 / V; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float sc = scale_of(m);
+          const float inv = 1.f / sc;
+          if (act[i]) {
+            float q[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
+            store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + v * V, q);
+            if (v % (128 / V) == 0) p.scale[(base + v * V) / 128] = sc;
+          }
+        }
+        top = max_nan(top, m);
+      }
+    }
+    if (QUANT == 2) {
+      top = slice_reduce<true>(Pair{top, 0.f}, s.tps, sm).a;
+      const float sc = scale_of(top);
+      const float inv = 1.f / sc;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (act[i]) {
+          float q[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
+          store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + (int64_t(i) * s.tps + lane) * V, q);
+        }
+      if (lane == 0 && slice < s.slices) p.scale[slice] = sc;
+    }
+  }
+}
+
+// Backward.  A CTA stays on one group of channels (blockIdx.x % groups), so a thread keeps its channels' dweight
+// in registers over all its rows; the CTA's sum goes to its row of scratch, and column_sums adds those rows.
+template <typename T, int VPT, bool GATE>
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
+  constexpr int V = Vec16<T>::n;
+  using VT = VecOf<T, V>;
+  __shared__ float sm[32][2];
+  extern __shared__ float acc[];   // [spc][L] when a CTA holds several slices
+  const int lane = threadIdx.x % s.tps, sub = threadIdx.x / s.tps;
+  const int64_t nv = s.L / V, total = p.rows * p.D;
+  const int64_t g = blockIdx.x % p.groups, blk = blockIdx.x / p.groups;
+  float dw[VPT][V] = {};
+  float wt[VPT][V];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int64_t v = int64_t(i) * s.tps + lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) wt[i][e] = v < nv ? __ldg(p.weight + g * s.L + v * V + e) : 0.f;
+  }
+  for (int64_t r0 = blk * s.spc; r0 < p.rows; r0 += nb * s.spc) {
+    const int64_t row = r0 + sub;
+    const int64_t base = row * p.D + g * s.L;
+    typename VT::R rx[VPT], rz[VPT], rg[VPT];
+    bool act[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = int64_t(i) * s.tps + lane, o = base + v * V;
+      act[i] = row < p.rows && v < nv && range_ok(o, V, total, p.status);
+      if (act[i]) {
+        rx[i] = VT::load(static_cast<const T*>(p.x) + o);
+        rg[i] = VT::load(static_cast<const T*>(p.dout) + o);
+        if (GATE) rz[i] = VT::load(static_cast<const T*>(p.other) + o);
+        else if (p.dh) rz[i] = VT::load(static_cast<const T*>(p.dh) + o);
+      }
+    }
+    float ss = 0.f, gh = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (act[i]) {
+        float x[V], z[V], d[V];
+        VT::get(rx[i], x);
+        VT::get(rg[i], d);
+        if (GATE) VT::get(rz[i], z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float h = GATE ? x[e] * (z[e] * sigmoid_of<T>(z[e])) : x[e];
+          ss = fmaf(h, h, ss);
+          gh = fmaf(d[e] * wt[i][e], h, gh);
+        }
+      }
+    const Pair r = slice_reduce<false>(Pair{ss, gh}, s.tps, sm);
+    const float rstd = rsqrtf(r.a / float(s.L) + p.eps);
+    const float m = r.b * rstd * rstd / float(s.L);   // mean(g xhat) rstd: dh = rstd (g - h m)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (act[i]) {
+        const int64_t o = base + (int64_t(i) * s.tps + lane) * V;
+        float x[V], z[V], d[V], dx[V], dz[V];
+        VT::get(rx[i], x);
+        VT::get(rg[i], d);
+        if (GATE || p.dh) VT::get(rz[i], z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float sg = GATE ? sigmoid_of<T>(z[e]) : 0.f;
+          const float h = GATE ? x[e] * (z[e] * sg) : x[e];
+          dw[i][e] = fmaf(d[e], h * rstd, dw[i][e]);
+          float dh = rstd * (d[e] * wt[i][e] - h * m);
+          if (GATE) {
+            dx[e] = dh * (z[e] * sg);
+            dz[e] = dh * x[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
+          } else {
+            dx[e] = p.dh ? dh + z[e] : dh;
+          }
+        }
+        VT::store(static_cast<T*>(p.dx) + o, dx);
+        if (GATE) VT::store(static_cast<T*>(p.dother) + o, dz);
+      }
+  }
+  if (!p.scratch) return;
+  float* out = p.scratch + blk * p.D + g * s.L;
+  if (s.spc == 1) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = int64_t(i) * s.tps + lane;
+      if (v < nv)
+#pragma unroll
+        for (int u = 0; u < V / 4; ++u)
+          *reinterpret_cast<float4*>(out + v * V + 4 * u) =
+              make_float4(dw[i][4 * u], dw[i][4 * u + 1], dw[i][4 * u + 2], dw[i][4 * u + 3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int64_t v = int64_t(i) * s.tps + lane;
+    if (v < nv)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[sub * s.L + v * V + e] = dw[i][e];
+  }
+  __syncthreads();
+  for (int64_t c = threadIdx.x; c < s.L; c += blockDim.x) {
+    float t = 0.f;
+    for (int i = 0; i < s.spc; ++i) t += acc[i * s.L + c];
+    out[c] = t;
+  }
+}
+
+__global__ void __launch_bounds__(1024) rms_dw_kernel(const float* scratch, int64_t rows, int64_t D, float* dweight) {
+  column_sums(scratch, rows, D, D, [&](int64_t c, float v) { dweight[c] = v; });
+}
+
+// Threads of a slice of nv vectors: one vector each up to 64 vectors, two up to 512, four above.
+int vectors_per_thread(int64_t nv) { return nv <= 64 ? 1 : nv <= 512 ? 2 : 4; }
+Shape shape_of(const RmsArgs& p, int64_t nv, int vpt) {
+  Shape s;
+  s.L = p.D / p.groups;
+  s.slices = p.rows * p.groups;
+  s.tps = 1;
+  while (int64_t(s.tps) * vpt < nv) s.tps *= 2;
+  s.spc = s.tps < kCta ? kCta / s.tps : 1;
+  return s;
+}
+constexpr int64_t kFwdCtas = 148 * 16;   // grid-stride over the rest
+constexpr int64_t kBwdThreads = 148 * 1024;   // resident threads of the backward at its 64-odd registers
+
+// CTAs per group of the backward: its scratch rows.
+int64_t bwd_blocks(int64_t rows, int64_t groups, int tps, int spc) {
+  const int64_t threads = int64_t(tps) * spc;
+  const int64_t cap = kBwdThreads / threads / groups, need = (rows + spc - 1) / spc;
+  const int64_t nb = need < cap ? need : cap;
+  return nb < 1 ? 1 : nb;
+}
+
+template <typename T, int VPT, int MODE, int QUANT>
+cudaError_t fwd(const RmsArgs& p, const Shape& s, cudaStream_t st) {
+  const int64_t need = (s.slices + s.spc - 1) / s.spc;
+  rms_fwd_kernel<T, VPT, MODE, QUANT><<<unsigned(need < kFwdCtas ? need : kFwdCtas), s.tps * s.spc, 0, st>>>(p, s);
+  return cudaGetLastError();
+}
+template <typename T, int VPT, int MODE>
+cudaError_t fwd_q(const RmsArgs& p, const Shape& s, cudaStream_t st) {
+  return p.quant_block == 0 ? fwd<T, VPT, MODE, 0>(p, s, st)
+         : p.quant_block > 0 ? fwd<T, VPT, MODE, 1>(p, s, st)
+                             : fwd<T, VPT, MODE, 2>(p, s, st);
+}
+template <typename T, int VPT>
+cudaError_t fwd_mode(const RmsArgs& p, const Shape& s, cudaStream_t st) {
+  return !p.other ? fwd_q<T, VPT, kPlain>(p, s, st) : p.gate ? fwd_q<T, VPT, kGate>(p, s, st) : fwd_q<T, VPT, kResidual>(p, s, st);
+}
+template <typename T, int VPT>
+cudaError_t bwd(const RmsArgs& p, const Shape& s, cudaStream_t st) {
+  const int64_t nb = bwd_blocks(p.rows, p.groups, s.tps, s.spc);
+  if (nb * p.groups > 2147483647) return cudaErrorInvalidValue;
+  const size_t smem = s.spc > 1 ? size_t(s.spc) * s.L * 4 : 0;   // at most 256 threads * 16 floats = 16 KiB
+  const dim3 grid(unsigned(nb * p.groups)), block(unsigned(s.tps * s.spc));
+  if (p.other) rms_bwd_kernel<T, VPT, true><<<grid, block, smem, st>>>(p, s, nb);
+  else rms_bwd_kernel<T, VPT, false><<<grid, block, smem, st>>>(p, s, nb);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.dweight) return e;
+  rms_dw_kernel<<<unsigned((p.D + 31) / 32), 1024, 0, st>>>(p.scratch, nb, p.D, p.dweight);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t run(const RmsArgs& p, bool backward, cudaStream_t st) {
+  const int64_t nv = p.D / p.groups / Vec16<T>::n;
+  const int vpt = vectors_per_thread(nv);
+  const Shape s = shape_of(p, nv, vpt);
+  if (s.tps > 1024) return cudaErrorInvalidValue;
+  if (backward) return vpt == 1 ? bwd<T, 1>(p, s, st) : vpt == 2 ? bwd<T, 2>(p, s, st) : bwd<T, 4>(p, s, st);
+  return vpt == 1 ? fwd_mode<T, 1>(p, s, st) : vpt == 2 ? fwd_mode<T, 2>(p, s, st) : fwd_mode<T, 4>(p, s, st);
+}
+cudaError_t run_dtype(const RmsArgs& p, int dtype, bool backward, cudaStream_t st) {
+  switch (dtype) {
+    case 0: return run<float>(p, backward, st);
+    case 1: return run<__nv_bfloat16>(p, backward, st);
+    case 2: return run<__half>(p, backward, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+// Enough for every dtype: the fewest threads per slice give the most rows of scratch.
+int64_t rms_scratch_floats(int64_t rows, int64_t D, int64_t groups) {
+  if (rows == 0 || D == 0) return 0;
+  int64_t most = 0;
+  for (int n : {4, 8}) {
+    const int64_t nv = D / groups / n;
+    RmsArgs p{};
+    p.rows = rows; p.D = D; p.groups = groups;
+    const Shape s = shape_of(p, nv, vectors_per_thread(nv));
+    const int64_t nb = bwd_blocks(rows, groups, s.tps, s.spc);
+    most = nb > most ? nb : most;
+  }
+  return most * D;
+}
+
+cudaError_t launch_rms_fwd(const RmsArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, false, s); }
+cudaError_t launch_rms_bwd(const RmsArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, true, s); }
+
+}  // namespace wkv7

@@ -10,13 +10,16 @@ stream.  The same entry points as the C ABI:
 * ``step(r, w, k, v, a, b, state, active=None, ...)`` -> y   (state updated in place)
 * ``gdn_map(q, k, g, beta, H, ...)`` -> dict(r, x, kw, a, b)   (gated-DeltaNet inputs -> WKV-7 inputs)
 * ``state_compose(S, P, U, ...)`` -> S P + U (or S P^T + U) per (b, h)   (context parallelism)
+* the state-space layer: ``conv_forward`` / ``conv_backward`` / ``conv_step`` (short causal convolution),
+  ``ssm_forward`` / ``ssm_backward`` / ``ssm_step`` (selective scan), ``rms_forward`` / ``rms_backward`` (RMS norm with
+  the residual's addition or a gate, e4m3 output)
 * ``workspace_bytes(B, T, H, dtype)``
 * ``device_status(clear=True)`` -> OK, ERR_TIMEOUT, ERR_BOUNDS or ERR_NONFINITE (synchronises the device)
 * ``use_build("release" | "debug")``: route every call through ``libwkv7.so`` (default) or its
   bounds-checked twin ``libwkv7_debug.so`` (same ABI; ``WKV7_BUILD=debug`` in the environment
   selects it at import)
 
-Tensors are [B,T,H,N] (token inputs), [B,H,N,N] fp32 (states), [B,T] uint8
+Tensors of the WKV-7 entry points are [B,T,H,N] (token inputs), [B,H,N,N] fp32 (states), [B,T] uint8
 (reset), [B] uint8 (active), all on one CUDA device and contiguous.  The head size N is 64; the
 token-order forward and the decode step also take N = 128 (the gated-delta-rule map's heads).  If the
 library is missing, importing this module raises: there is no fallback.
@@ -24,6 +27,7 @@ library is missing, importing this module raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -61,6 +65,25 @@ class Epilogue(ctypes.Structure):
 class Gdn(ctypes.Structure):
     """wkv7_gdn_t: key heads, the L2-normalisation guard and the scale taken into r."""
     _fields_ = [("Hk", ctypes.c_int64), ("eps", ctypes.c_float), ("r_scale", ctypes.c_float)]
+
+
+class Conv(ctypes.Structure):
+    """wkv7_conv_t: channels, taps, silu, fp32 filter [D,W] and bias [D], token stride of x."""
+    _fields_ = [("D", ctypes.c_int64), ("W", ctypes.c_int32), ("silu", ctypes.c_int32), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("x_ld", ctypes.c_int64)]
+
+
+class Ssm(ctypes.Structure):
+    """wkv7_ssm_t: groups, fp32 [H] decay rates, skip weights and dt bias, softplus, token strides."""
+    _fields_ = [("G", ctypes.c_int64), ("A", ctypes.c_void_p), ("D", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("softplus", ctypes.c_int32), ("x_ld", ctypes.c_int64), ("dt_ld", ctypes.c_int64),
+                ("b_ld", ctypes.c_int64), ("c_ld", ctypes.c_int64)]
+
+
+class Rms(ctypes.Structure):
+    """wkv7_rms_t: channels, slices of a row, fp32 weight [D], eps, how the second input enters, 8-bit blocks."""
+    _fields_ = [("D", ctypes.c_int64), ("groups", ctypes.c_int64), ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("gate", ctypes.c_int32), ("quant_block", ctypes.c_int32)]
 
 
 class WKV7Error(RuntimeError):
@@ -111,6 +134,18 @@ def _load(variant: str) -> ctypes.CDLL:
     L.wkv7_state_compose.argtypes = [dp, vp, vp, vp, vp, ctypes.c_int, vp]
     L.wkv7_gdn_map.restype = ctypes.c_int
     L.wkv7_gdn_map.argtypes = [dp, ctypes.POINTER(Gdn)] + [vp] * 10
+    for op, struct, calls in (("conv", Conv, (("forward", 6), ("backward", 11), ("step", 5))),
+                              ("ssm", Ssm, (("forward", 10), ("backward", 19), ("step", 8))),
+                              ("rms", Rms, (("forward", 6), ("backward", 9)))):
+        sp = ctypes.POINTER(struct)
+        for call, n in calls:
+            f = getattr(L, f"wkv7_{op}_{call}")
+            f.restype = ctypes.c_int
+            f.argtypes = [dp, sp] + [vp] * n
+        for size in ("scratch",) + (("workspace",) if op == "ssm" else ()):
+            f = getattr(L, f"wkv7_{op}_{size}_bytes")
+            f.restype = ctypes.c_size_t
+            f.argtypes = [dp, sp]
     return L
 
 
@@ -387,3 +422,290 @@ def state_compose(S, P, U, *, out=None, transpose: bool = False, stream=None, fl
                                   _stream(stream))
     _check(st, "wkv7_state_compose")
     return out
+
+
+# ------------------------------------------------------------------ state-space layer
+def _on_device(f):
+    """Run ``f`` on its first tensor's device and on ``stream`` (default: that device's current stream); what it
+    allocates belongs to that stream."""
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kw):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise ValueError(f"{f.__name__}: tensors must be on a CUDA device")
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"{f.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
+            with torch.cuda.stream(stream):
+                return f(x, *args, **kw)
+        if x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return f(x, *args, **kw)
+        return f(x, *args, **kw)
+    return call
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
+    """Address of a contiguous tensor of the given shape and dtype on ``like``'s device (None stays None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got strides {t.stride()} for shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, shape, lead: int, like: torch.Tensor):
+    """(address, token stride) of token rows [B,T,..] (``lead`` = 2) or [B,..] (``lead`` = 1) whose rows are dense;
+    the rows themselves may be slices of wider ones.  The stride is 0 where there is only one row."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be {like.dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    st, width = t.stride(), 1
+    ok = True
+    for i in range(t.dim() - 1, lead - 1, -1):
+        ok = ok and (t.shape[i] == 1 or st[i] == width)
+        width *= t.shape[i]
+    ld, n = None, 1
+    for i in range(lead - 1, -1, -1):
+        if t.shape[i] != 1:
+            ld = st[i] // n if ld is None else ld
+            ok = ok and st[i] == ld * n
+        n *= t.shape[i]
+    if not ok or (ld is not None and ld < width):
+        raise ValueError(f"{name}: only the distance between tokens may differ from a dense tensor's, got strides {st} for "
+                         f"shape {tuple(t.shape)}")
+    return t.data_ptr(), ld or 0
+
+
+def _mask(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor):
+    if t is not None and t.dtype == torch.bool:
+        t = t.view(torch.uint8)
+    return _dense(t, name, shape, torch.uint8, like)
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
+    if t is None:
+        return torch.empty(shape, device=like.device, dtype=dtype)
+    _dense(t, name, shape, dtype, like)
+    return t
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(n: int, like: torch.Tensor):
+    return torch.empty(max(int(n), 16), device=like.device, dtype=torch.uint8)
+
+
+def _now(like: torch.Tensor):
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _conv_args(x, weight, bias, silu, lead, flags):
+    shape = tuple(x.shape)
+    if len(shape) != lead + 1 or weight.dim() != 2:
+        raise ValueError(f"expected x [B,{'T,' if lead == 2 else ''}D] and weight [D,W], got {shape} and {tuple(weight.shape)}")
+    B, T, D = shape[0], shape[1] if lead == 2 else 1, shape[-1]
+    px, ld = _rows(x, "x", shape, lead, x)
+    cv = Conv(D, int(weight.shape[1]), 1 if silu else 0, _dense(weight, "weight", (D, weight.shape[1]), torch.float32, x),
+              _dense(bias, "bias", (D,), torch.float32, x), ld)
+    return make_desc(B, T, 0, x.dtype, flags=flags), cv, px, (B, T, D, int(weight.shape[1]))
+
+
+@_on_device
+def conv_forward(x, weight, bias=None, s0=None, reset=None, *, silu: bool = True, y=None, s_out=None,
+                 want_state: bool = True, flags: int = 0):
+    """Short causal convolution per channel: u_t = bias + sum_j weight[:, W-1-j] x_{t-j}, y = silu(u) (or u).
+
+    x [B,T,D] (token rows may be slices of wider ones), weight fp32 [D,W] with W = 2..4, bias fp32 [D]; s0 [B,W-1,D]
+    holds the inputs before the row (oldest first), reset [B,T] cuts the taps before a token.  Returns (y, s_out)."""
+    d, cv, px, (B, T, D, W) = _conv_args(x, weight, bias, silu, 2, flags)
+    y = _out(y, "y", (B, T, D), x.dtype, x)
+    if s_out is not None or want_state:
+        s_out = _out(s_out, "s_out", (B, W - 1, D), x.dtype, x)
+    st = lib().wkv7_conv_forward(d, cv, px, _dense(s0, "s0", (B, W - 1, D), x.dtype, x), _mask(reset, "reset", (B, T), x),
+                                 y.data_ptr(), _addr(s_out), _now(x))
+    _check(st, "wkv7_conv_forward")
+    return y, s_out
+
+
+@_on_device
+def conv_backward(x, weight, dy, bias=None, s0=None, reset=None, dsT=None, *, silu: bool = True, grads=None,
+                  want_params: bool = True, want_ds0: bool = True, flags: int = 0) -> Dict[str, torch.Tensor]:
+    """Reverse mode of ``conv_forward`` from dy [B,T,D] and dsT (gradient of s_out, or None): dict of dx, and, where
+    wanted, fp32 dweight [D,W], dbias [D] and ds0 [B,W-1,D]."""
+    d, cv, px, (B, T, D, W) = _conv_args(x, weight, bias, silu, 2, flags)
+    g = dict(grads) if grads is not None else {}
+    g["dx"] = _out(g.get("dx"), "dx", (B, T, D), x.dtype, x)
+    if want_params:
+        g["dweight"] = _out(g.get("dweight"), "dweight", (D, W), torch.float32, x)
+        g["dbias"] = _out(g.get("dbias"), "dbias", (D,), torch.float32, x)
+    if want_ds0:
+        g["ds0"] = _out(g.get("ds0"), "ds0", (B, W - 1, D), x.dtype, x)
+    tmp = _scratch(lib().wkv7_conv_scratch_bytes(d, cv), x) if want_params else None
+    st = lib().wkv7_conv_backward(d, cv, px, _dense(s0, "s0", (B, W - 1, D), x.dtype, x), _mask(reset, "reset", (B, T), x),
+                                  _dense(dy, "dy", (B, T, D), x.dtype, x), _dense(dsT, "dsT", (B, W - 1, D), x.dtype, x),
+                                  g["dx"].data_ptr(), _addr(g.get("dweight")), _addr(g.get("dbias")), _addr(g.get("ds0")),
+                                  _addr(tmp), _now(x))
+    _check(st, "wkv7_conv_backward")
+    return g
+
+
+@_on_device
+def conv_step(x, weight, state, bias=None, active=None, *, silu: bool = True, y=None, flags: int = 0):
+    """One decode token of the convolution: x [B,D], state [B,W-1,D] shifted in place.  Returns y [B,D]."""
+    d, cv, px, (B, _, D, W) = _conv_args(x, weight, bias, silu, 1, flags)
+    y = _out(y, "y", (B, D), x.dtype, x)
+    st = lib().wkv7_conv_step(d, cv, px, _dense(state, "state", (B, W - 1, D), x.dtype, x), _mask(active, "active", (B,), x),
+                              y.data_ptr(), _now(x))
+    _check(st, "wkv7_conv_step")
+    return y
+
+
+def _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, lead, algo, flags):
+    if x.dim() != lead + 2 or b.dim() != lead + 2 or x.shape[-1] != N_HEAD:
+        raise ValueError(f"expected x [B,{'T,' if lead == 2 else ''}H,{N_HEAD}] and b, c [B,{'T,' if lead == 2 else ''}G,N], got "
+                         f"{tuple(x.shape)} and {tuple(b.shape)}")
+    lead_shape = tuple(x.shape[:lead])
+    B, T, H = lead_shape[0], lead_shape[1] if lead == 2 else 1, int(x.shape[lead])
+    G, N = int(b.shape[lead]), int(b.shape[-1])
+    px, x_ld = _rows(x, "x", lead_shape + (H, N_HEAD), lead, x)
+    pt, t_ld = _rows(dt, "dt", lead_shape + (H,), lead, x)
+    pb, b_ld = _rows(b, "b", lead_shape + (G, N), lead, x)
+    pc, c_ld = _rows(c, "c", lead_shape + (G, N), lead, x)
+    sp = Ssm(G, *(_dense(t, n, (H,), torch.float32, x) for t, n in ((A, "A"), (D, "D"), (dt_bias, "dt_bias"))),
+             1 if softplus else 0, x_ld, t_ld, b_ld, c_ld)
+    return make_desc(B, T, H, x.dtype, algo, N=N, flags=flags), sp, (px, pt, pb, pc), (B, T, H, G, N)
+
+
+@_on_device
+def ssm_forward(x, dt, A, b, c, D=None, dt_bias=None, s0=None, reset=None, *, softplus: bool = True, y=None, s_out=None,
+                workspace=None, need_workspace: bool = True, want_state: bool = True, algo: str = "auto", flags: int = 0):
+    """Selective state space scan: d = softplus(dt + dt_bias), S_t = exp(d A) S_{t-1} + d x_t b_t^T, y_t = S_t c_t + D x_t.
+
+    x [B,T,H,64], dt [B,T,H], b, c [B,T,G,N] (H / G consecutive heads share a group; N = 64 or 128; token rows may be
+    slices of wider ones), A, D, dt_bias fp32 [H], s0 fp32 [B,H,64,N], reset [B,T].  Returns (y, s_out, workspace)."""
+    d, sp, ptrs, (B, T, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 2, algo, flags)
+    y = _out(y, "y", (B, T, H, N_HEAD), x.dtype, x)
+    if s_out is not None or want_state:
+        s_out = _out(s_out, "s_out", (B, H, N_HEAD, N), torch.float32, x)
+    need = int(lib().wkv7_ssm_workspace_bytes(d, sp)) if workspace is not None or need_workspace else 0
+    if workspace is None and need_workspace:
+        workspace = _scratch(need, x)
+    elif workspace is not None and workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"the workspace must hold {need} bytes")
+    st = lib().wkv7_ssm_forward(d, sp, *ptrs, _dense(s0, "s0", (B, H, N_HEAD, N), torch.float32, x),
+                                _mask(reset, "reset", (B, T), x), y.data_ptr(), _addr(s_out),
+                                None if workspace is None else _dense(workspace, "workspace", workspace.shape, workspace.dtype, x),
+                                _now(x))
+    _check(st, "wkv7_ssm_forward")
+    return y, s_out, workspace
+
+
+@_on_device
+def ssm_backward(x, dt, A, b, c, dy, workspace, D=None, dt_bias=None, s0=None, reset=None, dsT=None, *,
+                 softplus: bool = True, grads=None, want_ds0: bool = True, algo: str = "auto",
+                 flags: int = 0) -> Dict[str, torch.Tensor]:
+    """Reverse mode of ``ssm_forward`` from its workspace, dy [B,T,H,64] and dsT (gradient of s_out, or None): dict of
+    dx, ddt, db, dc, fp32 dA, dD, ddt_bias (the last two where D and dt_bias are given) and, where wanted, ds0."""
+    d, sp, ptrs, (B, T, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 2, algo, flags)
+    g = dict(grads) if grads is not None else {}
+    shapes = {"dx": (B, T, H, N_HEAD), "ddt": (B, T, H), "db": (B, T, G, N), "dc": (B, T, G, N)}
+    for n, shape in shapes.items():
+        g[n] = _out(g.get(n), n, shape, x.dtype, x)
+    for n, on in (("dA", True), ("dD", D is not None), ("ddt_bias", dt_bias is not None)):
+        if on:
+            g[n] = _out(g.get(n), n, (H,), torch.float32, x)
+    if want_ds0:
+        g["ds0"] = _out(g.get("ds0"), "ds0", (B, H, N_HEAD, N), torch.float32, x)
+    need = int(lib().wkv7_ssm_workspace_bytes(d, sp))
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"the backward needs the forward's workspace of {need} bytes")
+    tmp = _scratch(lib().wkv7_ssm_scratch_bytes(d, sp), x)
+    st = lib().wkv7_ssm_backward(d, sp, *ptrs, _dense(s0, "s0", (B, H, N_HEAD, N), torch.float32, x),
+                                 _mask(reset, "reset", (B, T), x), _dense(dy, "dy", (B, T, H, N_HEAD), x.dtype, x),
+                                 _dense(dsT, "dsT", (B, H, N_HEAD, N), torch.float32, x),
+                                 _dense(workspace, "workspace", workspace.shape, workspace.dtype, x),
+                                 *(_addr(g.get(n)) for n in ("dx", "ddt", "db", "dc", "dA", "dD", "ddt_bias", "ds0")),
+                                 tmp.data_ptr(), _now(x))
+    _check(st, "wkv7_ssm_backward")
+    return g
+
+
+@_on_device
+def ssm_step(x, dt, A, b, c, state, D=None, dt_bias=None, active=None, *, softplus: bool = True, y=None, flags: int = 0):
+    """One decode token of the scan: x [B,H,64], dt [B,H], b, c [B,G,N], state fp32 [B,H,64,N] in place.  Returns y."""
+    d, sp, ptrs, (B, _, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 1, "auto", flags)
+    y = _out(y, "y", (B, H, N_HEAD), x.dtype, x)
+    st = lib().wkv7_ssm_step(d, sp, *ptrs, _dense(state, "state", (B, H, N_HEAD, N), torch.float32, x),
+                             _mask(active, "active", (B,), x), y.data_ptr(), _now(x))
+    _check(st, "wkv7_ssm_step")
+    return y
+
+
+def _rms_args(x, weight, eps, groups, gate, quant_block, flags):
+    if x.dim() < 1:
+        raise ValueError("x must have a channel dimension")
+    D = int(x.shape[-1])
+    rows = x.numel() // D if D > 0 else 0
+    rn = Rms(D, int(groups), _dense(weight, "weight", (D,), torch.float32, x), float(eps), 1 if gate else 0, int(quant_block))
+    return make_desc(rows, 1, 0, x.dtype, flags=flags), rn, rows
+
+
+@_on_device
+def rms_forward(x, weight, eps: float, *, residual=None, gate=None, groups: int = 1, quant_block: int = 0, h=None, out=None,
+                scale=None, flags: int = 0) -> Dict[str, torch.Tensor]:
+    """RMS norm over ``groups`` equal slices of the last dimension: out = h / sqrt(mean(h^2) + eps) * weight with
+    h = x, x + residual (stored, and returned as "h") or x * silu(gate).
+
+    quant_block = 0: dict with "out" in x's dtype.  128: e4m3 "q" and one fp32 "scale" per 128 channels; -1: one scale
+    per slice (value = q * scale)."""
+    if residual is not None and gate is not None:
+        raise ValueError("rms_forward takes a residual or a gate, not both")
+    other = residual if residual is not None else gate
+    d, rn, _ = _rms_args(x, weight, eps, groups, gate is not None, quant_block, flags)
+    D = int(x.shape[-1])
+    px = _dense(x, "x", x.shape, x.dtype, x)
+    r = {}
+    if residual is not None:
+        r["h"] = _out(h, "h", x.shape, x.dtype, x)
+    elif h is not None:
+        raise ValueError("h is an output of the residual's addition only")
+    if quant_block:
+        r["q"] = _out(out, "out", x.shape, torch.float8_e4m3fn, x)
+        r["scale"] = _out(scale, "scale", tuple(x.shape[:-1]) + ((D // 128) if quant_block > 0 else int(groups),), torch.float32, x)
+    else:
+        r["out"] = _out(out, "out", x.shape, x.dtype, x)
+    st = lib().wkv7_rms_forward(d, rn, px, _dense(other, "residual or gate", x.shape, x.dtype, x), _addr(r.get("h")),
+                                (r["q"] if quant_block else r["out"]).data_ptr(), _addr(r.get("scale")), _now(x))
+    _check(st, "wkv7_rms_forward")
+    return r
+
+
+@_on_device
+def rms_backward(x, weight, dout, eps: float, *, gate=None, dh=None, groups: int = 1, grads=None, want_params: bool = True,
+                 flags: int = 0) -> Dict[str, torch.Tensor]:
+    """Reverse mode of ``rms_forward`` (without 8-bit output): dict of dx, fp32 dweight and, with a gate, dgate.  After a
+    residual's addition x is the stored sum "h"; dx is then the gradient of both summands, and ``dh``, the gradient
+    that reaches the sum directly, is added in."""
+    d, rn, _ = _rms_args(x, weight, eps, groups, gate is not None, 0, flags)
+    g = dict(grads) if grads is not None else {}
+    px = _dense(x, "x", x.shape, x.dtype, x)
+    g["dx"] = _out(g.get("dx"), "dx", x.shape, x.dtype, x)
+    if gate is not None:
+        g["dgate"] = _out(g.get("dgate"), "dgate", x.shape, x.dtype, x)
+    if want_params:
+        g["dweight"] = _out(g.get("dweight"), "dweight", (x.shape[-1],), torch.float32, x)
+    tmp = _scratch(lib().wkv7_rms_scratch_bytes(d, rn), x) if want_params else None
+    st = lib().wkv7_rms_backward(d, rn, px, _dense(gate, "gate", x.shape, x.dtype, x),
+                                 _dense(dout, "dout", x.shape, x.dtype, x), _dense(dh, "dh", x.shape, x.dtype, x),
+                                 g["dx"].data_ptr(), _addr(g.get("dgate")), _addr(g.get("dweight")), _addr(tmp), _now(x))
+    _check(st, "wkv7_rms_backward")
+    return g
