@@ -341,7 +341,8 @@ def _run_own(s):
         y, s_out = wkv7.conv_forward(s["x"], s["weight"], s["bias"], s["s0"], s["reset"], silu=case["silu"])
         if mode == "forward":
             return {"y": y, "s_out": s_out}
-        g = wkv7.conv_backward(s["x"], s["weight"], s["dy"], s["bias"], s["s0"], s["reset"], s["dsT"], silu=case["silu"])
+        g = wkv7.conv_backward(s["x"], s["weight"], s["dy"], s["bias"], s["s0"], s["reset"], s["dsT"], silu=case["silu"],
+                               want_ds0=s["s0"] is not None)
         return {"y": y, "s_out": s_out, **{n: g[n] for n in ("dx", "dweight", "dbias", "ds0") if g.get(n) is not None}}
     args = [s[n] for n in ("x", "dt", "A", "b", "c")]
     if mode == "step":
