@@ -7,7 +7,9 @@
 // E = <state after the chunk, gradient of it> the paths that leave the chunk.  A reset ends every path, so the sum runs
 // to the end of t's segment, E belongs to the last segment only, and the reset token's own decay has no gradient.  The
 // paths that neither start nor end at t cancel in the difference, so it is summed in fp64; the path from a token to
-// itself is in neither sum (it would cancel too, at a far larger size where little is remembered).
+// itself is in neither sum (it would cancel too, at a far larger size where little is remembered).  What leaves the chunk
+// is in E and in col: the chunked backward hands that part of col over on its own (`far`) and E without it, so that the
+// same numbers are added here and cancel exactly.
 //   dL/dd_t = A dL/da_t + col_t + own_t,   own_t = (x . dy)(b . c);   ddt = dL/dd sigmoid(dt + bias)
 //
 // One warp per (b, h, chunk), 4 tokens per lane; latency-bound (a few microseconds), 16 bytes read per token-head.
@@ -16,7 +18,7 @@
 namespace wkv7 {
 namespace {
 
-template <typename T>
+template <typename T, bool CHUNKED>
 __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmScratch sc, float* part) {
   const int lane = threadIdx.x & 31;
   const int64_t nc = chunks_of(p.T), tp = nc * kSsmChunk;
@@ -30,7 +32,12 @@ __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmSc
   const float4 xd = *reinterpret_cast<const float4*>(p.scratch + sc.xdy + o);
   const float owns[4] = {own.x, own.y, own.z, own.w}, xds[4] = {xd.x, xd.y, xd.z, xd.w};
   float d[4] = {}, sg[4] = {};
-  double v[4], suf[4];
+  double v[4], suf[4], cs[4] = {}, leave = 0.0;
+  float fr[4] = {};
+  if (CHUNKED) {
+    const float4 f4 = *reinterpret_cast<const float4*>(p.scratch + sc.far + o);
+    fr[0] = f4.x; fr[1] = f4.y; fr[2] = f4.z; fr[3] = f4.w;
+  }
   unsigned rst = 0, cut = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -39,21 +46,26 @@ __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmSc
       float raw;
       d[i] = step_of<T>(p, b * p.T + t0 + i, h, &raw);
       sg[i] = p.softplus ? 1.f / (1.f + expf(-raw)) : 1.f;
-      v[i] = rows[i] - double(d[i]) * cols[i];
+      cs[i] = CHUNKED ? cols[i] + double(fr[i]) : cols[i];
+      v[i] = rows[i] - double(d[i]) * cs[i];
+      if (CHUNKED) leave += double(d[i]) * double(fr[i]);
       if (p.reset && p.reset[b * p.T + t0 + i]) rst |= 1u << i;
     }
   }
   cut = rst >> 1;   // token i ends its segment where token i + 1 is a reset
   const unsigned next = __shfl_down_sync(0xffffffffu, rst, 1);
   if (lane < 31 && (next & 1u)) cut |= 8u;
-  if (lane == 31) v[3] += reinterpret_cast<const double*>(p.scratch + sc.anchor)[w];   // the chunk's last token carries E
+  if (CHUNKED)
+#pragma unroll
+    for (int s = 16; s; s >>= 1) leave += __shfl_xor_sync(0xffffffffu, leave, s);
+  if (lane == 31) v[3] += leave + reinterpret_cast<const double*>(p.scratch + sc.anchor)[w];   // the chunk's last token carries E
   segmented_suffix(v, cut, suf);
   double dA = 0.0, dB = 0.0, dD = 0.0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (t0 + i < p.T) {
       const double da = (rst >> i & 1u) ? 0.0 : suf[i];
-      const double g = (double(A) * da + cols[i] + double(owns[i])) * double(sg[i]);
+      const double g = (double(A) * da + cs[i] + double(owns[i])) * double(sg[i]);
       static_cast<T*>(p.ddt)[(b * p.T + t0 + i) * p.H + h] = Elt<T>::from_f32(float(g));
       dA += double(d[i]) * da;
       dB += g;
@@ -95,9 +107,12 @@ cudaError_t launch_ssm_decay(const SsmArgs& p, int dtype, bool chunked, cudaStre
   const unsigned grid = unsigned((warps + 7) / 8);
   float* part = p.scratch + sc.part;
   switch (dtype) {
-    case 0: decay_kernel<float><<<grid, 256, 0, s>>>(p, sc, part); break;
-    case 1: decay_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p, sc, part); break;
-    case 2: decay_kernel<__half><<<grid, 256, 0, s>>>(p, sc, part); break;
+    case 0: decay_kernel<float, false><<<grid, 256, 0, s>>>(p, sc, part); break;
+    case 1:
+      if (chunked) decay_kernel<__nv_bfloat16, true><<<grid, 256, 0, s>>>(p, sc, part);
+      else decay_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(p, sc, part);
+      break;
+    case 2: decay_kernel<__half, false><<<grid, 256, 0, s>>>(p, sc, part); break;
     default: return cudaErrorInvalidValue;
   }
   cudaError_t e = cudaGetLastError();
@@ -113,12 +128,29 @@ SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool c
   auto take = [&](int64_t n) { const int64_t at = o; o += (n + 3) / 4 * 4; return at; };
   s.row = take(2 * tok);
   s.col = take(2 * tok);
+  if (chunked) s.far = take(tok);
   s.own = take(tok);
   s.xdy = take(tok);
   s.anchor = take(2 * B * H * nc);
   s.part = take(3 * B * H * nc);
   if (chunked) {
     s.dstate = take(B * H * nc * state);
+    // heads of a group per CTA: as few splits as leave every SM its share within a tenth
+    const int64_t units = B * nc * G, hg = H / G;
+    s.splits = 1;
+    double best = 1e300;
+    for (int64_t k = 1; k <= hg && k <= 32; k *= 2) {
+      const int64_t per = (hg + k - 1) / k, rounds = (units * k + 147) / 148;
+      const double cost = double(rounds * per) + 0.05 * double(units * k) / 148.0;   // a part's sums cost about 1/20 head
+      if (cost < best * 0.97) {
+        best = cost;
+        s.splits = k;
+      }
+    }
+    if (s.splits > 1) {
+      s.db_part = take(s.splits * B * T * G * N);
+      s.dc_part = take(s.splits * B * T * G * N);
+    }
   } else {
     s.dstate = take(2 * B * H * nc * state);
     s.state_t = take(2 * B * H * (nc + 1) * state);

@@ -1,0 +1,234 @@
+// Tensor-core side of the chunked selective scan: swizzled tiles, their matrix descriptors, tensor maps, bounded
+// waits, and the per-token decay factors of a chunk.  Beside tc05.cuh (allocation, fences, MMA issue).
+//
+// Tiles hold rows of 64 bf16 (128 bytes) in the 128-byte swizzle that TMA writes: 16-byte piece j of row r sits at
+// r * 128 + ((j ^ (r & 7)) << 4), 8 rows make one 1024-byte atom.  A tile serves both ways round:
+//   * rows = M or N, columns = K ("K-major"): 8-row groups 1024 bytes apart, one MMA's K = 16 is 32 bytes along the row;
+//   * rows = K, columns = M or N ("MN-major"): one MMA's K = 16 is two 8-row groups, 2048 bytes along; columns beyond 64
+//     are in the next tile.
+#pragma once
+
+#include "ssm.cuh"
+#include "tc05.cuh"
+
+namespace wkv7 {
+namespace stc {
+
+constexpr int kQ = kSsmChunk;                  // tokens of a chunk = rows of a token tile
+constexpr int kTileBytes = kQ * 128;           // [128][64] bf16
+
+__device__ __forceinline__ int swz(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t mn_block_bytes) {
+  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((mn_block_bytes >> 4) & 0x3FFFu) << 16)   // start; distance of 64-column blocks
+         | (uint64_t(1024 >> 4) << 32)                                                           // distance of 8-row groups
+         | (uint64_t(1) << 46) | (uint64_t(2) << 61);                                            // version, 128-byte swizzle
+}
+// Operand `step` (K = 16 each) of a K-major operand whose 64-column tiles are `tile_bytes` apart, from the descriptor of
+// its start (the address sits in the low bits, in units of 16 bytes).
+__device__ __forceinline__ uint64_t k_step(uint64_t d, int step, uint32_t tile_bytes = kTileBytes) {
+  return d + (((step >> 2) * tile_bytes + (step & 3) * 32) >> 4);
+}
+// The same of an MN-major one (K along the rows).
+__device__ __forceinline__ uint64_t mn_step(uint64_t d, int step) { return d + ((step * 2048) >> 4); }
+
+// D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc], kind::f16
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(0u)
+      : "memory");
+}
+
+// 16 columns of 32 lanes: thread l of warp w reaches lane 32 (w % 4) + l.  While MMAs run, one such move holds up its
+// quadrant for about 80 cycles whether it moves 8 columns or 32 (measured), so narrower ones cost the same.
+__device__ __forceinline__ void ld16(uint32_t taddr, float (&v)[16]) { tc::ld_32x32b_x16(taddr, v); }
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// 2^x, 2^-22 relative; results below the normal range are zero
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 2^(hi + lo): the integer part goes into the exponent, so that only a fraction is rounded
+__device__ __forceinline__ float ex2_pair(float hi, float lo) {
+  const float n = fmaxf(rintf(hi), -200.f);
+  return ex2((hi - n) + lo) * ex2(n);   // the second is exact (0 below 2^-126, inf above 2^127)
+}
+
+// ---- pairs of bf16 in a register
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack(uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+// v = hi + mid (+ lo): bf16 parts, 8 significant bits each.
+__device__ __forceinline__ uint32_t split(float2& v) {
+  const uint32_t h = pack(v.x, v.y);
+  v = sub2(v, unpack(h));
+  return h;
+}
+
+// ---- waits: bounded, and given up by everyone once one has run out.  A poll may suspend the thread for a millisecond
+// (spinning warps take issue slots and instruction fetches from the working ones).
+__device__ __forceinline__ bool try_wait_ms(unsigned long long* bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool wait_slow(unsigned long long* bar, unsigned parity, int* dead, int* status) {
+  const unsigned long long t0 = global_ns();
+  while (!try_wait_ms(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(dead)) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *reinterpret_cast<volatile int*>(dead) = 1;
+      atomicOr(status, kStatusWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+struct Wait {
+  int* dead;          // shared: set once a wait has run out
+  int* status;        // the device status word
+  __device__ __forceinline__ bool operator()(unsigned long long* bar, unsigned parity) const {   // one thread
+    return try_wait_ms(bar, parity) || wait_slow(bar, parity, dead, status);
+  }
+  __device__ __forceinline__ bool warp(unsigned long long* bar, unsigned parity) const {         // all lanes, one answer
+    return __all_sync(0xffffffffu, (*this)(bar, parity));
+  }
+};
+__device__ __forceinline__ void arrive(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// ---- token tiles by TMA: {64, heads or groups, T, B}, box {64, 1, 128, 1}; tokens past T read as zeros
+struct TileMaps {
+  CUtensorMap x, b, c, dy;
+};
+// A barrier of `n` warps that gives up with everyone else: each use toggles the phase.
+struct WarpBarrier {
+  unsigned long long* bar;
+  unsigned phase;
+  __device__ __forceinline__ bool operator()(const Wait& wait) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive(bar);
+    const bool ok = wait.warp(bar, phase);
+    phase ^= 1u;
+    return ok;
+  }
+};
+
+// ---- decays of one chunk.  Lambda_t: sum of log2 decays from the chunk's start up to and with token t, summed in fp64
+// and kept as a pair of floats; r_t: a reset at or before t in the chunk.  Everything is zero behind the row's end.
+struct Decays {
+  float hi[kQ], lo[kQ];   // Lambda_t
+  float d[kQ];            // step
+  float in[kQ];           // 2^Lambda_t, 0 where r_t: what is left at t of the state that enters the chunk
+  float out[kQ];          // 2^(Lambda_end - Lambda_t), 0 if a reset follows: what is left of token t at the chunk's end
+  float rel[kQ];          // Lambda_t - Lambda at the start of t's block of 32
+  int start[kQ];          // first token of t's segment in the chunk
+  // Off the diagonal 32 x 32 blocks the decay is a product of two factors, both relative to the row block w:
+  float far[192];         // forward: d_s 2^(Lambda before block w - Lambda_s) for the tokens s before block w = 1, 2, 3;
+                          // backward: 2^(Lambda_t - Lambda at the end of block w) for the tokens t after block w = 0, 1, 2
+  float total;            // 2^Lambda_end, 0 with a reset
+  int resets;             // any reset in the chunk
+  int growing;            // any decay above one
+  int pad;
+};
+
+// 2^(Lambda_a - Lambda_b) of two tokens (or of the chunk's start: zero).
+__device__ __forceinline__ float decay_between(float ahi, float alo, float bhi, float blo) {
+  return ex2_pair(ahi - bhi, alo - blo);
+}
+
+// The raw steps and resets of tokens 32 k + lane of chunk c (loads only, so that they can be under way early).
+struct RawSteps {
+  float v[4];
+  unsigned rst;   // bit k
+  __device__ __forceinline__ void load(const SsmArgs& p, int64_t b, int64_t h, int64_t c) {
+    const int64_t t0 = c * kQ + (threadIdx.x & 31), bt = b * p.T + t0;
+    rst = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool ok = t0 + 32 * k < p.T;
+      v[k] = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dt)[(bt + 32 * k) * p.dt_ld + h]) : 0.f;
+      if (ok && p.reset && p.reset[bt + 32 * k]) rst |= 1u << k;
+    }
+  }
+};
+
+// One warp fills `o` for chunk c: 32 tokens at a time, in rolled loops (see the chunk kernel on code size).
+__device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, bool backward, Decays& o) {
+  const int lane = threadIdx.x & 31;
+  const double A2 = double(A) * 1.4426950408889634074;
+  double before = 0.0;      // Lambda at the start of the block
+  int last = -1;            // last reset before the block
+  bool grow = false;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    const int t = 32 * k + lane;
+    const float v = (k == 0 ? raw.v[0] : k == 1 ? raw.v[1] : k == 2 ? raw.v[2] : raw.v[3]) + bias;
+    const float d = c * kQ + t < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
+    double sum = double(d) * A2;
+    grow |= sum > 0.0;
+#pragma unroll 1
+    for (int s = 1; s < 32; s *= 2) {
+      const double u = __shfl_up_sync(0xffffffffu, sum, s);
+      if (lane >= s) sum += u;
+    }
+    const double l = before + sum;
+    const unsigned rst = __ballot_sync(0xffffffffu, raw.rst >> k & 1u), upto = rst & (0xffffffffu >> (31 - lane));
+    const int prev = upto ? 32 * k + 31 - __clz(upto) : last;
+    const float hi = float(l), lo = float(l - double(hi));
+    o.hi[t] = hi;
+    o.lo[t] = lo;
+    o.d[t] = d;
+    o.rel[t] = float(sum);
+    o.in[t] = prev < 0 ? ex2_pair(hi, lo) : 0.f;
+    o.start[t] = prev < 0 ? 0 : prev;
+    before = __shfl_sync(0xffffffffu, l, 31);
+    if (rst) last = 32 * k + 31 - __clz(rst);
+  }
+  const float ehi = float(before), elo = float(before - double(ehi));
+  __syncwarp();
+#pragma unroll 1
+  for (int t = lane; t < kQ; t += 32) o.out[t] = t >= last ? decay_between(ehi, elo, o.hi[t], o.lo[t]) : 0.f;
+#pragma unroll 1
+  for (int k = 0; k < 6; ++k) {
+    if (!backward) {
+      const int w = k < 1 ? 1 : k < 3 ? 2 : 3, t = 32 * (k - w * (w - 1) / 2) + lane, m = 32 * w - 1;
+      o.far[32 * k + lane] = o.d[t] * decay_between(o.hi[m], o.lo[m], o.hi[t], o.lo[t]);
+    } else {
+      const int w = k < 3 ? 0 : k < 5 ? 1 : 2, t = 32 * (k < 3 ? k + 1 : k < 5 ? k - 1 : 3) + lane, m = 32 * w + 31;
+      o.far[32 * k + lane] = decay_between(o.hi[t], o.lo[t], o.hi[m], o.lo[m]);
+    }
+  }
+  const unsigned any_grow = __ballot_sync(0xffffffffu, grow);
+  if (lane == 0) {
+    o.total = last < 0 ? ex2_pair(ehi, elo) : 0.f;
+    o.resets = last >= 0;
+    o.growing = any_grow != 0;
+  }
+}
+
+}  // namespace stc
+}  // namespace wkv7

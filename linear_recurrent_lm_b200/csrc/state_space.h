@@ -82,12 +82,15 @@ struct SsmArgs {
 // Parts of the backward's scratch, as offsets in fp32 elements (16-byte aligned); `d`: fp64 values.
 struct SsmScratch {
   int64_t row, col;        // d [B,H,nc*128] per token: see ssm_decay.cu
+  int64_t far;             // [B,H,nc*128] per token: CHUNKED: the part of col that leaves the chunk (not in `col` then)
   int64_t own, xdy;        // [B,H,nc*128] per token: (x . dy)(b . c) and x . dy
-  int64_t anchor;          // d [B,H,nc] <state after the chunk, gradient of it>
+  int64_t anchor;          // d [B,H,nc] <state after the chunk, gradient of it> (CHUNKED: without what `far` starts)
   int64_t part;            // [B,H,nc,3] partial dA, dD, ddt_bias
   int64_t dstate;          // [B,H,nc] gradient of the state after each chunk (SCAN: d, transposed)
   int64_t state_t;         // SCAN: d [B,H,nc+1] states before each chunk and the last, transposed as dstate
   int64_t dcp, dbp;        // SCAN: d [B,T,H,N] the past's part of dc and db per head
+  int64_t db_part, dc_part;   // CHUNKED: [splits][B,T,G,N] sums over the heads of a split, where there are several
+  int64_t splits;             // CHUNKED: parts that a group's heads are cut into
   int64_t total;
 };
 SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool chunked);

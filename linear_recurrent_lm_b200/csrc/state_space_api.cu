@@ -5,6 +5,8 @@
 
 #include <initializer_list>
 
+#include "ssm_chunk.h"
+#include "ssm_tc.cuh"
 #include "state_space.h"
 #include "wkv7.h"
 
@@ -102,7 +104,7 @@ wkv7_status_t check_ssm(const wkv7_desc_t* d, const wkv7_ssm_t* sp, wkv7::SsmArg
   if (!sp) return WKV7_ERR_NULL;
   if (d->N != 64 && d->N != 128) return WKV7_ERR_UNSUPPORTED;
   if (d->algo != WKV7_ALGO_AUTO && d->algo != WKV7_ALGO_SCAN && d->algo != WKV7_ALGO_CHUNKED) return WKV7_ERR_UNSUPPORTED;
-  if (d->algo == WKV7_ALGO_CHUNKED) return WKV7_ERR_UNSUPPORTED;
+  if (d->algo == WKV7_ALGO_CHUNKED && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
   if (sp->G < 1 || d->H % sp->G != 0) return WKV7_ERR_UNSUPPORTED;
   // every byte count of inputs, states, checkpoints and scratch, and every grid, fits
   const int64_t nc = (d->T + wkv7::kSsmChunk - 1) / wkv7::kSsmChunk;
@@ -124,6 +126,8 @@ wkv7_status_t check_ssm(const wkv7_desc_t* d, const wkv7_ssm_t* sp, wkv7::SsmArg
   if (d->B > 0 && d->H > 0 && !sp->A) return WKV7_ERR_NULL;
   return check_ptrs(false, {sp->A, sp->D, sp->dt_bias}, 4);
 }
+
+bool chunked(const wkv7_desc_t* d) { return d->dtype == WKV7_BF16 && d->algo != WKV7_ALGO_SCAN; }
 
 // ------------------------------------------------------------------ norm
 wkv7_status_t check_rms(const wkv7_desc_t* d, const wkv7_rms_t* rn, wkv7::RmsArgs* a, bool sizes_only = false) {
@@ -229,14 +233,21 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const
   if (wkv7::device_status_ptr(&a.status) != cudaSuccess) return WKV7_ERR_CUDA;
   a.x = x; a.dt = dt; a.b = b; a.c = c; a.s0 = s0; a.reset = reset; a.y = y; a.s_out = s_out;
   a.ckpt = static_cast<float*>(workspace);
-  const cudaError_t e = wkv7::launch_ssm_scan_fwd(a, d->dtype, s);
+  cudaError_t e;
+  if (chunked(d)) {
+    wkv7::stc::TileMaps tm;
+    if (!wkv7::encode_ssm_maps(a, false, &tm)) return WKV7_ERR_CUDA;
+    e = wkv7::launch_ssm_chunk_fwd(a, tm, s);
+  } else {
+    e = wkv7::launch_ssm_scan_fwd(a, d->dtype, s);
+  }
   return finish(d, e, {{y, n, d->dtype}, {s_out, st, WKV7_F32}}, a.status, s);
 }
 
 size_t wkv7_ssm_scratch_bytes(const wkv7_desc_t* d, const wkv7_ssm_t* sp) {
   wkv7::SsmArgs a;
   if (check_ssm(d, sp, &a, true) != WKV7_OK || d->T == 0) return 0;
-  return size_t(wkv7::ssm_scratch(d->B, d->T, d->H, sp->G, d->N, false).total) * 4;
+  return size_t(wkv7::ssm_scratch(d->B, d->T, d->H, sp->G, d->N, chunked(d)).total) * 4;
 }
 
 wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const void* x, const void* dt, const void* b,
@@ -261,8 +272,15 @@ wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, cons
   a.ckpt = static_cast<float*>(const_cast<void*>(workspace));
   a.dx = dx; a.ddt = ddt; a.db = db; a.dc = dc; a.dA = dA; a.dD = dD; a.ddt_bias = ddt_bias; a.ds0 = ds0;
   a.scratch = static_cast<float*>(scratch);
-  cudaError_t e = wkv7::launch_ssm_scan_bwd(a, d->dtype, s);
-  if (e == cudaSuccess) e = wkv7::launch_ssm_decay(a, d->dtype, false, s);
+  cudaError_t e;
+  if (chunked(d)) {
+    wkv7::stc::TileMaps tm;
+    if (!wkv7::encode_ssm_maps(a, true, &tm)) return WKV7_ERR_CUDA;
+    e = wkv7::launch_ssm_chunk_bwd(a, tm, s);
+  } else {
+    e = wkv7::launch_ssm_scan_bwd(a, d->dtype, s);
+  }
+  if (e == cudaSuccess) e = wkv7::launch_ssm_decay(a, d->dtype, chunked(d), s);
   return finish(d, e,
                 {{dx, n, d->dtype}, {ddt, units * d->T, d->dtype}, {db, nb, d->dtype}, {dc, nb, d->dtype}, {dA, d->H, WKV7_F32},
                  {dD, d->H, WKV7_F32}, {ddt_bias, d->H, WKV7_F32}, {ds0, st, WKV7_F32}},

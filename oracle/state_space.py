@@ -105,7 +105,8 @@ def ssm_forward(x, dt, A, b, c, D=None, dt_bias=None, s0=None, reset=None, softp
     return (y, S, states) if keep else (y, S)
 
 
-def ssm_backward(x, dt, A, b, c, dy, D=None, dt_bias=None, s0=None, reset=None, dsT=None, softplus=True):
+def ssm_backward(x, dt, A, b, c, dy, D=None, dt_bias=None, s0=None, reset=None, dsT=None, softplus=True, sizes=False):
+    """``sizes``: with every input but dt and A non-negative, the sums of the absolute terms behind each gradient."""
     _, _, states = ssm_forward(x, dt, A, b, c, D, dt_bias, s0, reset, softplus, keep=True)
     x, dt, A, b, c, dy, D, dt_bias, dsT = _f64(x, dt, A, b, c, dy, D, dt_bias, dsT)
     B, T, H, P = x.shape
@@ -127,7 +128,7 @@ def ssm_backward(x, dt, A, b, c, dy, D=None, dt_bias=None, s0=None, reset=None, 
         f = np.exp(d[:, t] * A)
         da = f * np.einsum("bhpn,bhpn->bh", before, dS)
         g["dx"][:, t] = d[:, t, :, None] * du + (0.0 if D is None else D[:, None] * dy[:, t])
-        ddt = (A * da + np.einsum("bhp,bhp->bh", x[:, t], du)) * sg[:, t]
+        ddt = ((np.abs(A) if sizes else A) * da + np.einsum("bhp,bhp->bh", x[:, t], du)) * sg[:, t]
         g["ddt"][:, t] = ddt
         g["dA"] += (d[:, t] * da).sum(0)
         g["ddt_bias"] += ddt.sum(0)

@@ -5,8 +5,10 @@ wider tensors, other streams, captured graphs, and the whole layer run as it is 
 Tolerances, all relative to the reference's RMS and beyond the half step that storing in a 16-bit type costs:
 * fp32 arithmetic (every kernel but the chunked scan): an output is a chain of at most a few hundred fp32
   operations on terms of at most some tens of RMS, each off by 2^-24: 512 * 2^-24 * 3 = 9e-5, taken as 1e-4;
-* chunked scan, 16-bit outputs: its products round one operand to bf16 (2^-9 at most), so an output that adds up terms
-  of 5 RMS in all is off by 1e-2 at worst: 2e-2 with both products of a gradient;
+* chunked scan, 16-bit outputs: at most two factors of each term of an output's sum are rounded to bf16 (2^-9 each at
+  most), so an element is off by no more than 2^-8 of the sum of its terms' absolute values, which the oracle gives on
+  the absolute values of the inputs; and as the roundings are independent (1.7e-3 of a value on average, three of them
+  with the output's own), all elements together by 1.7e-3 * sqrt(3) = 3e-3 of the output's norm: 4e-3;
 * chunked scan, fp32 outputs (states, parameter gradients): operands split in three bf16 parts: as fp32 arithmetic.
 """
 from __future__ import annotations
@@ -19,7 +21,7 @@ from tests.metrics import err_rms, err_rms_excess
 
 pytestmark = pytest.mark.gpu
 
-FP32, CHUNKED = 1e-4, 2e-2
+FP32, CHUNKED, CHUNKED_NORM = 1e-4, 2.0 ** -8, 4e-3
 DT = ("f32", "bf16", "f16")
 
 
@@ -55,6 +57,17 @@ def _close(got, ref, dtype, tol, what=""):
     assert np.isfinite(got).all(), what
     err = err_rms(got, ref) if dtype == "f32" else err_rms_excess(got, ref, dtype)
     assert err <= tol, (what, err)
+
+
+def _close_chunked(got, ref, size, what=""):
+    """bf16 outputs of the chunked scan: ``size`` holds the sums of the absolute terms of each element."""
+    got = _f64(got)
+    assert got.shape == ref.shape and np.isfinite(got).all(), what
+    half = np.abs(ref) * 2.0 ** -8 + 1e-30                     # storing the result: half a step of bf16
+    worst = np.max((np.abs(got - ref) - half) / (size + 1e-30))
+    assert worst <= CHUNKED, (what, worst)
+    norm = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+    assert norm <= CHUNKED_NORM, (what, norm)
 
 
 # ------------------------------------------------------------------ convolution
@@ -156,24 +169,42 @@ def _ssm_case(rng, dtype, B, T, H, G, N, reset="some", state=True, strided=True,
     return dev, ref
 
 
+def _sizes(ref, softplus, dy=None, dsT=None):
+    """Sums of the absolute terms of the outputs: the oracle on absolute values."""
+    a = {n: v if n in ("dt", "A", "dt_bias", "reset") or v is None else np.abs(v) for n, v in ref.items()}
+    if not softplus:
+        step = ref["dt"] + (0.0 if ref["dt_bias"] is None else ref["dt_bias"])   # may be negative: keep its size in the terms
+        scale = np.where(step < 0, -1.0, 1.0)
+        a["x"] = a["x"] * scale[..., None]
+    if dy is None:
+        return S.ssm_forward(**a, softplus=softplus)[0]
+    return S.ssm_backward(dy=np.abs(dy), dsT=None if dsT is None else np.abs(dsT), softplus=softplus, sizes=True, **a)
+
+
 def _ssm_check(W, rng, dtype, algo, dev, ref, softplus=True):
-    B, T, H = ref["x"].shape[:3]
-    tol = CHUNKED if algo == "chunked" else FP32
+    chunked = algo == "chunked"
     y, s, ws = W.ssm_forward(**dev, softplus=softplus, algo=algo)
     yo, so = S.ssm_forward(**ref, softplus=softplus)
-    _close(y, yo, dtype, tol, "y")
+    if chunked:
+        _close_chunked(y, yo, np.abs(_sizes(ref, softplus)), "y")
+    else:
+        _close(y, yo, dtype, FP32, "y")
     _close(s, so, "f32", FP32, "s_out")
     dy, dy64 = _dev(rng.standard_normal(ref["x"].shape), dtype)
     ds, ds64 = _dev(rng.standard_normal(so.shape).astype(np.float32)) if ref["s0"] is not None else (None, None)
     g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, softplus=softplus, algo=algo, **dev)
     go = S.ssm_backward(dy=dy64, dsT=ds64, softplus=softplus, **ref)
+    size = _sizes(ref, softplus, dy64, ds64) if chunked else None
     assert set(g) == {"dx", "ddt", "db", "dc", "dA", "ds0"} | ({"dD", "ddt_bias"} if dev["D"] is not None else set())
     for n in g:
         fp32 = n in ("dA", "dD", "ddt_bias", "ds0")
-        _close(g[n], go[n], "f32" if fp32 else dtype, FP32 if fp32 else tol, n)
+        if chunked and not fp32:
+            _close_chunked(g[n], go[n], np.abs(size[n]), n)
+        else:
+            _close(g[n], go[n], "f32" if fp32 else dtype, FP32, n)
 
 
-FORMS = [("f32", "scan"), ("bf16", "scan"), ("f16", "scan")]
+FORMS = [("f32", "scan"), ("bf16", "scan"), ("f16", "scan"), ("bf16", "chunked")]
 
 
 @pytest.mark.parametrize("dtype,algo", FORMS)
@@ -200,6 +231,35 @@ def test_ssm_edges(W, dtype, algo, case):
     _ssm_check(W, rng, dtype, algo, dev, ref, softplus=case != "linear_dt")
 
 
+@pytest.mark.parametrize("shape", ((2, 1000, 40, 2, 64), (1, 2500, 6, 1, 128), (3, 700, 64, 1, 128)))
+def test_ssm_chunked_equals_scan_on_larger_shapes(W, shape):
+    """More heads than SMs, long rows of few heads: the two forms against each other, all outputs."""
+    import torch
+    B, T, H, G, N = shape
+    rng = np.random.default_rng(240)
+    dev, _ = _ssm_case(rng, "bf16", B, T, H, G, N)
+    dy = torch.randn(B, T, H, 64, device="cuda").bfloat16()
+    ds = torch.randn(B, H, 64, N, device="cuda")
+    r = {}
+    for algo in ("scan", "chunked"):
+        y, s, ws = W.ssm_forward(**dev, algo=algo)
+        r[algo] = {"y": y, "s_out": s, **W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo=algo, **dev)}
+        y2, s2, _ = W.ssm_forward(**dev, algo=algo, need_workspace=False)
+        _near(y2, y, "y without a workspace")
+        _close(s2, _f64(s), "f32", FP32, "s_out without a workspace")
+    for n, t in r["chunked"].items():
+        if t.dtype == torch.float32:
+            _close(t, _f64(r["scan"][n]), "f32", FP32, n)
+        else:
+            _near(t, r["scan"][n], n)
+
+
+def _near(got, want, what=""):
+    """bf16 results of two forms of the scan, each stored once more than _close_chunked counts."""
+    norm = ((got.double() - want.double()).norm() / want.double().norm()).item()
+    assert norm <= CHUNKED_NORM, (what, norm)
+
+
 @pytest.mark.parametrize("dtype,algo", FORMS)
 def test_ssm_split_equals_one_call(W, dtype, algo):
     """Two chained calls, forward and backward, against the single one, cut inside and at the border of a chunk."""
@@ -210,19 +270,19 @@ def test_ssm_split_equals_one_call(W, dtype, algo):
     ds, _ = _dev(rng.standard_normal((2, 4, 64, 64)).astype(np.float32))
     y, s, ws = W.ssm_forward(**dev, algo=algo)
     g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo=algo, **dev)
-    tol = CHUNKED if algo == "chunked" else FP32
+    same = _near if algo == "chunked" else lambda a, b, n: _close(a, _f64(b), dtype, FP32, n)
     for cut in (128, 77):
         part = lambda a, z: {n: (v[:, a:z].contiguous() if n in ("x", "dt", "b", "c", "reset") else v) for n, v in dev.items()}   # noqa: E731
         first, second = part(0, cut), part(cut, 290)
         ya, sa, wa = W.ssm_forward(**first, algo=algo)
         second["s0"] = sa
         yb, sb, wb = W.ssm_forward(**second, algo=algo)
-        _close(torch.cat([ya, yb], 1), _f64(y), dtype, tol, "y")
+        same(torch.cat([ya, yb], 1), y, "y")
         _close(sb, _f64(s), "f32", FP32, "s")
         gb = W.ssm_backward(dy=dy[:, cut:].contiguous(), workspace=wb, dsT=ds, algo=algo, **second)
         ga = W.ssm_backward(dy=dy[:, :cut].contiguous(), workspace=wa, dsT=gb["ds0"], algo=algo, **first)
         for n in ("dx", "ddt", "db", "dc"):
-            _close(torch.cat([ga[n], gb[n]], 1), _f64(g[n]), dtype, tol, n)
+            same(torch.cat([ga[n], gb[n]], 1), g[n], n)
         _close(ga["ds0"], _f64(g["ds0"]), "f32", FP32, "ds0")
         for n in ("dA", "dD", "ddt_bias"):
             _close(ga[n] + gb[n], _f64(g[n]), "f32", FP32, n)
@@ -249,7 +309,7 @@ def test_ssm_steps_follow_the_forward(W, dtype, N, G):
     assert not torch.equal(state[active], keep[active])
 
 
-@pytest.mark.parametrize("algo", ("scan",))
+@pytest.mark.parametrize("algo", ("scan", "chunked"))
 def test_ssm_repeats_bit_for_bit(W, algo):
     import torch
     rng = np.random.default_rng(270)
