@@ -429,27 +429,56 @@ cudaError_t run_n(const SsmArgs& p, const TileMaps& tm, const ChunkOp& op, cudaS
 
 }  // namespace
 
+// Runs that a row's chunks are cut into: with fewer rows of heads than SMs, as many as fill them, of at least 4 chunks.  A
+// cut row is walked twice, first for the state that each run leaves (without the outputs' work), then from it on, so it
+// takes three runs to gain.
+int64_t ssm_segments(int64_t units, int64_t nc) {
+  const int64_t fit = units > 0 ? 148 / units : 1, most = nc / 4, k = fit < most ? fit : most;
+  return k >= 3 ? k : 1;
+}
+int64_t ssm_segment_floats(int64_t B, int64_t T, int64_t H, int N) {
+  const int64_t k = ssm_segments(B * H, chunks_of(T));
+  return k > 1 ? B * H * k * (64 * N + 1) : 0;
+}
+
+namespace {
+template <bool OUT, bool REV>
+cudaError_t walk(const SsmArgs& p, const TileMaps& tm, ChunkOp op, float* seg, cudaStream_t s) {
+  const int64_t nc = chunks_of(p.T), k = seg ? ssm_segments(p.B * p.H, nc) : 1;
+  op.per_segment = (nc + k - 1) / k;
+  op.segments = (nc + op.per_segment - 1) / op.per_segment;
+  if (op.segments > 1) {
+    op.seg_state = seg;
+    op.seg_decay = seg + p.B * p.H * op.segments * 64 * p.N;
+    ChunkOp first = op;
+    first.local = true;
+    first.states = nullptr;
+    first.last = nullptr;
+    const cudaError_t e = run_n<false, REV>(p, tm, first, s);
+    if (e != cudaSuccess) return e;
+  }
+  return run_n<OUT, REV>(p, tm, op, s);
+}
+}  // namespace
+
 cudaError_t launch_ssm_chunk_fwd(const SsmArgs& p, const TileMaps& tm, cudaStream_t s) {
+  const int64_t nc = chunks_of(p.T);
   ChunkOp op{};
-  op.segments = 1;
-  op.per_segment = chunks_of(p.T);
   op.init = p.s0;
   op.states = p.ckpt;
-  op.stride = chunks_of(p.T) + 1;
+  op.stride = nc + 1;
   op.last = p.s_out;
-  return run_n<true, false>(p, tm, op, s);
+  return walk<true, false>(p, tm, op, p.ckpt ? p.ckpt + p.B * p.H * (nc + 1) * 64 * p.N : nullptr, s);
 }
 
 // The gradient of the state after each chunk into the backward's scratch, and of the initial state.
-cudaError_t launch_ssm_chunk_dstate(const SsmArgs& p, const TileMaps& tm, float* dstate, cudaStream_t s) {
+cudaError_t launch_ssm_chunk_dstate(const SsmArgs& p, const TileMaps& tm, float* dstate, float* seg, cudaStream_t s) {
   ChunkOp op{};
-  op.segments = 1;
-  op.per_segment = chunks_of(p.T);
   op.init = p.dsT;
   op.states = dstate;
   op.stride = chunks_of(p.T);
   op.last = p.ds0;
-  return run_n<false, true>(p, tm, op, s);
+  return walk<false, true>(p, tm, op, seg, s);
 }
 
 }  // namespace wkv7

@@ -22,7 +22,7 @@ struct ChunkOp {
 };
 
 cudaError_t launch_ssm_chunk_fwd(const SsmArgs& p, const stc::TileMaps& tm, cudaStream_t s);
-cudaError_t launch_ssm_chunk_dstate(const SsmArgs& p, const stc::TileMaps& tm, float* dstate, cudaStream_t s);
+cudaError_t launch_ssm_chunk_dstate(const SsmArgs& p, const stc::TileMaps& tm, float* dstate, float* seg, cudaStream_t s);
 // Everything of the backward but the decays' gradients (which follow from the scalars it leaves in scratch).
 cudaError_t launch_ssm_chunk_bwd(const SsmArgs& p, const stc::TileMaps& tm, cudaStream_t s);
 // Tensor maps of the bf16 token tensors (see ssm_tc.cuh); false if the driver refuses one.

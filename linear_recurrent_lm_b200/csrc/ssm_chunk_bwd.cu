@@ -514,7 +514,7 @@ cudaError_t run(const SsmArgs& p, const SsmScratch& sc, const TileMaps& tm, cuda
 
 cudaError_t launch_ssm_chunk_bwd(const SsmArgs& p, const TileMaps& tm, cudaStream_t s) {
   const SsmScratch sc = ssm_scratch(p.B, p.T, p.H, p.G, p.N, true);
-  const cudaError_t e = launch_ssm_chunk_dstate(p, tm, p.scratch + sc.dstate, s);
+  const cudaError_t e = launch_ssm_chunk_dstate(p, tm, p.scratch + sc.dstate, p.scratch + sc.seg, s);
   if (e != cudaSuccess) return e;
   return p.N == 128 ? run<128>(p, sc, tm, s) : run<64>(p, sc, tm, s);
 }

@@ -135,6 +135,7 @@ SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool c
   s.part = take(3 * B * H * nc);
   if (chunked) {
     s.dstate = take(B * H * nc * state);
+    s.seg = take(ssm_segment_floats(B, T, H, N));
     // heads of a group per CTA: as few splits as leave every SM its share within a tenth
     const int64_t units = B * nc * G, hg = H / G;
     s.splits = 1;

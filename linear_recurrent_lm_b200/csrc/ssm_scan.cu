@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
   for (int64_t pos0 = 0; pos0 < T_; pos0 += kTile, buf ^= 1) {
     const int n = int(min64(kTile, T_ - pos0));
     if (pos0 + kTile < T_) fetch(pos0 + kTile);
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const F f = s_f[buf][i];
       const int64_t t = token(pos0 + i);

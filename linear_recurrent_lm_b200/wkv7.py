@@ -425,6 +425,7 @@ def state_compose(S, P, U, *, out=None, transpose: bool = False, stream=None, fl
 
 
 # ------------------------------------------------------------------ state-space layer
+# Calls of single tokens last a few microseconds on the GPU, so the checks here are kept short.
 def _on_device(f):
     """Run ``f`` on its first tensor's device and on ``stream`` (default: that device's current stream); what it
     allocates belongs to that stream."""
@@ -437,7 +438,7 @@ def _on_device(f):
                 raise ValueError(f"{f.__name__}: the stream is on {stream.device}, the tensors on {x.device}")
             with torch.cuda.stream(stream):
                 return f(x, *args, **kw)
-        if x.get_device() != torch.cuda.current_device():
+        if x.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(x.device):
                 return f(x, *args, **kw)
         return f(x, *args, **kw)
@@ -448,9 +449,9 @@ def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tenso
     """Address of a contiguous tensor of the given shape and dtype on ``like``'s device (None stays None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, got strides {t.stride()} for shape {tuple(t.shape)}")
@@ -459,34 +460,34 @@ def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tenso
 
 def _rows(t: torch.Tensor, name: str, shape, lead: int, like: torch.Tensor):
     """(address, token stride) of token rows [B,T,..] (``lead`` = 2) or [B,..] (``lead`` = 1) whose rows are dense;
-    the rows themselves may be slices of wider ones.  The stride is 0 where there is only one row."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != like.dtype:
+    the rows themselves may be slices of wider ones.  The stride is 0 where it is the row's size."""
+    if t.shape != shape or t.dtype != like.dtype:
         raise ValueError(f"{name} must be {like.dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {like.device}")
     if t.is_contiguous():
         return t.data_ptr(), 0
     st, width = t.stride(), 1
     ok = True
     for i in range(t.dim() - 1, lead - 1, -1):
-        ok = ok and (t.shape[i] == 1 or st[i] == width)
-        width *= t.shape[i]
+        ok = ok and (shape[i] == 1 or st[i] == width)
+        width *= shape[i]
     ld, n = None, 1
     for i in range(lead - 1, -1, -1):
-        if t.shape[i] != 1:
+        if shape[i] != 1:
             ld = st[i] // n if ld is None else ld
             ok = ok and st[i] == ld * n
-        n *= t.shape[i]
+        n *= shape[i]
     if not ok or (ld is not None and ld < width):
         raise ValueError(f"{name}: only the distance between tokens may differ from a dense tensor's, got strides {st} for "
-                         f"shape {tuple(t.shape)}")
+                         f"shape {tuple(shape)}")
     return t.data_ptr(), ld or 0
 
 
 def _mask(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor):
-    if t is not None and t.dtype == torch.bool:
-        t = t.view(torch.uint8)
-    return _dense(t, name, shape, torch.uint8, like)
+    if t is None:
+        return None
+    return _dense(t.view(torch.uint8) if t.dtype == torch.bool else t, name, shape, torch.uint8, like)
 
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
@@ -501,22 +502,29 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _scratch(n: int, like: torch.Tensor):
-    return torch.empty(max(int(n), 16), device=like.device, dtype=torch.uint8)
+    return torch.empty(max(n, 16), device=like.device, dtype=torch.uint8)
 
 
 def _now(like: torch.Tensor):
-    return torch.cuda.current_stream().cuda_stream
+    """The current stream of ``like``'s device, which is the current device."""
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _code(dtype) -> int:
+    code = DTYPE_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"expected one of {list(DTYPE_CODE)}, got {dtype}")
+    return code
 
 
 def _conv_args(x, weight, bias, silu, lead, flags):
-    shape = tuple(x.shape)
+    shape = x.shape
     if len(shape) != lead + 1 or weight.dim() != 2:
-        raise ValueError(f"expected x [B,{'T,' if lead == 2 else ''}D] and weight [D,W], got {shape} and {tuple(weight.shape)}")
-    B, T, D = shape[0], shape[1] if lead == 2 else 1, shape[-1]
+        raise ValueError(f"expected x [B,{'T,' if lead == 2 else ''}D] and weight [D,W], got {tuple(shape)} and {tuple(weight.shape)}")
+    B, T, D, W = shape[0], shape[1] if lead == 2 else 1, shape[-1], weight.shape[1]
     px, ld = _rows(x, "x", shape, lead, x)
-    cv = Conv(D, int(weight.shape[1]), 1 if silu else 0, _dense(weight, "weight", (D, weight.shape[1]), torch.float32, x),
-              _dense(bias, "bias", (D,), torch.float32, x), ld)
-    return make_desc(B, T, 0, x.dtype, flags=flags), cv, px, (B, T, D, int(weight.shape[1]))
+    cv = Conv(D, W, 1 if silu else 0, _dense(weight, "weight", (D, W), torch.float32, x), _dense(bias, "bias", (D,), torch.float32, x), ld)
+    return Desc(B, T, 0, N_HEAD, _code(x.dtype), 0, flags), cv, px, (B, T, D, W)
 
 
 @_on_device
@@ -574,15 +582,15 @@ def _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, lead, algo, flags):
         raise ValueError(f"expected x [B,{'T,' if lead == 2 else ''}H,{N_HEAD}] and b, c [B,{'T,' if lead == 2 else ''}G,N], got "
                          f"{tuple(x.shape)} and {tuple(b.shape)}")
     lead_shape = tuple(x.shape[:lead])
-    B, T, H = lead_shape[0], lead_shape[1] if lead == 2 else 1, int(x.shape[lead])
-    G, N = int(b.shape[lead]), int(b.shape[-1])
+    B, T, H = lead_shape[0], lead_shape[1] if lead == 2 else 1, x.shape[lead]
+    G, N = b.shape[lead], b.shape[-1]
     px, x_ld = _rows(x, "x", lead_shape + (H, N_HEAD), lead, x)
     pt, t_ld = _rows(dt, "dt", lead_shape + (H,), lead, x)
     pb, b_ld = _rows(b, "b", lead_shape + (G, N), lead, x)
     pc, c_ld = _rows(c, "c", lead_shape + (G, N), lead, x)
     sp = Ssm(G, *(_dense(t, n, (H,), torch.float32, x) for t, n in ((A, "A"), (D, "D"), (dt_bias, "dt_bias"))),
              1 if softplus else 0, x_ld, t_ld, b_ld, c_ld)
-    return make_desc(B, T, H, x.dtype, algo, N=N, flags=flags), sp, (px, pt, pb, pc), (B, T, H, G, N)
+    return Desc(B, T, H, N, _code(x.dtype), ALGO_CODE[algo], flags), sp, (px, pt, pb, pc), (B, T, H, G, N)
 
 
 @_on_device
@@ -653,10 +661,10 @@ def ssm_step(x, dt, A, b, c, state, D=None, dt_bias=None, active=None, *, softpl
 def _rms_args(x, weight, eps, groups, gate, quant_block, flags):
     if x.dim() < 1:
         raise ValueError("x must have a channel dimension")
-    D = int(x.shape[-1])
+    D = x.shape[-1]
     rows = x.numel() // D if D > 0 else 0
-    rn = Rms(D, int(groups), _dense(weight, "weight", (D,), torch.float32, x), float(eps), 1 if gate else 0, int(quant_block))
-    return make_desc(rows, 1, 0, x.dtype, flags=flags), rn, rows
+    rn = Rms(D, groups, _dense(weight, "weight", (D,), torch.float32, x), eps, 1 if gate else 0, quant_block)
+    return Desc(rows, 1, 0, N_HEAD, _code(x.dtype), 0, flags), rn, rows
 
 
 @_on_device
@@ -671,7 +679,7 @@ def rms_forward(x, weight, eps: float, *, residual=None, gate=None, groups: int 
         raise ValueError("rms_forward takes a residual or a gate, not both")
     other = residual if residual is not None else gate
     d, rn, _ = _rms_args(x, weight, eps, groups, gate is not None, quant_block, flags)
-    D = int(x.shape[-1])
+    D = x.shape[-1]
     px = _dense(x, "x", x.shape, x.dtype, x)
     r = {}
     if residual is not None:
