@@ -3,7 +3,7 @@
 // A reset at t cuts the taps before t: zeroing the window of earlier inputs there is the same thing, and the
 // window after the last token is the state that a decode step continues from.
 //
-// HBM-bound: x is read and y written once (2 D elements per token).  One thread owns one 16-byte vector of
+// HBM-bound: x is read and y written once (2 D elements per token).  One thread owns four
 // channels and a run of tokens, so the window stays in registers and every input element is loaded once per run
 // plus W - 1 tokens of run-in (in L2: the neighbouring run has just read them).  The run length is chosen so
 // that the grid still fills the machine: long runs save run-in, short ones keep small calls parallel.
@@ -14,8 +14,11 @@
 namespace wkv7 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kRunThreads = 128;   // decode step; forward and backward
+constexpr int kV = 4;            // channels of a thread: 8 per thread (16-byte loads of bf16) took 108 registers and 0.142 ms
+                                 // for B=8 T=4096 D=2304
 constexpr int kBatch = 4;        // tokens whose loads are issued together
+static_assert(kBatch == 4, "the tokens of a batch are picked by hand where one is a reset");
 constexpr int kNoReset = 1 << 20;
 
 template <int W, int V>
@@ -69,11 +72,11 @@ __device__ __forceinline__ int load_window(const ConvArgs& p, int64_t b, int64_t
 }
 
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p, int64_t run, int64_t runs) {
-  constexpr int V = Vec16<T>::n;
+__global__ void __launch_bounds__(kRunThreads) conv_fwd_kernel(const ConvArgs p, int64_t run, int64_t runs) {
+  constexpr int V = kV;
   using VT = VecOf<T, V>;
   const int64_t nv = p.D / V;
-  const int64_t id = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t id = int64_t(blockIdx.x) * kRunThreads + threadIdx.x;
   const int64_t br = id / nv, d0 = (id - br * nv) * V, b = br / runs;
   if (b >= p.B) return;
   const int64_t t0 = (br - b * runs) * run, t1 = min64(t0 + run, p.T);
@@ -82,37 +85,65 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p, in
   load_window<T, W, V>(p, b, t0, d0, win);
   const T* x = static_cast<const T*>(p.x) + b * p.T * p.x_ld + d0;
   T* y = static_cast<T*>(p.y) + b * p.T * p.D + d0;
-  for (int64_t t = t0; t < t1; t += kBatch) {
-    typename VT::R raw[kBatch];
-    bool cut[kBatch];
+  const uint8_t* reset = p.reset ? p.reset + b * p.T : nullptr;
+  auto token = [&](const typename VT::R& raw, int64_t t) {   // u_t from its input and the window, which moves on
+    float v[V], u[V];
+    VT::get(raw, v);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (t + i < t1) {
-        raw[i] = VT::load(x + (t + i) * p.x_ld);
-        cut[i] = p.reset && p.reset[b * p.T + t + i];
-      }
+    for (int e = 0; e < V; e += 2) {
+      float2 a = fma2(make_float2(w[0][e], w[0][e + 1]), make_float2(v[e], v[e + 1]), make_float2(bias[e], bias[e + 1]));
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (t + i >= t1) break;
-      float v[V], u[V];
-      VT::get(raw[i], v);
-      if (cut[i])
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-          for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        u[e] = fmaf(w[0][e], v[e], bias[e]);
-#pragma unroll
-        for (int j = 1; j < W; ++j) u[e] = fmaf(w[j][e], win[j - 1][e], u[e]);
-        if (SILU) u[e] *= sigmoid_of<T>(u[e]);
-#pragma unroll
-        for (int j = W - 2; j > 0; --j) win[j][e] = win[j - 1][e];
-        win[0][e] = v[e];
-      }
-      if (range_ok((b * p.T + t + i) * p.D + d0, V, p.B * p.T * p.D, p.status)) VT::store(y + (t + i) * p.D, u);
+      for (int j = 1; j < W; ++j)
+        a = fma2(make_float2(w[j][e], w[j][e + 1]), make_float2(win[j - 1][e], win[j - 1][e + 1]), a);
+      u[e] = SILU ? a.x * sigmoid_of<T>(a.x) : a.x;
+      u[e + 1] = SILU ? a.y * sigmoid_of<T>(a.y) : a.y;
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+#pragma unroll
+      for (int j = W - 2; j > 0; --j) win[j][e] = win[j - 1][e];
+      win[0][e] = v[e];
+    }
+    if (range_ok((b * p.T + t) * p.D + d0, V, p.B * p.T * p.D, p.status)) VT::store(y + t * p.D, u);
+  };
+  int64_t t = t0;
+  typename VT::R next[kBatch];   // loads run one batch ahead
+  if (t + kBatch <= t1)
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) next[i] = VT::load(x + (t + i) * p.x_ld);
+  for (; t + kBatch <= t1; t += kBatch) {
+    typename VT::R raw[kBatch];
+    unsigned cut = 0;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+    if (t + 2 * kBatch <= t1)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) next[i] = VT::load(x + (t + kBatch + i) * p.x_ld);
+    if (reset)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) cut |= reset[t + i] ? 1u << i : 0u;
+    if (cut == 0) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) token(raw[i], t + i);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kBatch; ++i) {
+        if (cut >> i & 1u)
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < V; ++e) win[j][e] = 0.f;
+        token(i == 0 ? raw[0] : i == 1 ? raw[1] : i == 2 ? raw[2] : raw[3], t + i);
+      }
+    }
+  }
+  for (; t < t1; ++t) {
+    if (reset && reset[t])
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) win[j][e] = 0.f;
+    token(VT::load(x + t * p.x_ld), t);
   }
   if (p.s_out && t1 == p.T)
 #pragma unroll
@@ -124,15 +155,13 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p, in
 // cuts, dw[j] = sum_t du_t x_{t-j}, dbias = sum_t du_t.  A thread owns 4 channels (the filter's gradient stays in
 // registers beside the windows) and a run of tokens; it walks W - 1 tokens past its run for the gradients that
 // reach back into it.  The filter's partial sums per run go to scratch and are added by column_sums.
-constexpr int kBwdV = 4;
-constexpr int kBwdThreads = 128;
 
 template <typename T, int W, bool SILU>
-__global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(const ConvArgs p, int64_t run, int64_t runs) {
-  constexpr int V = kBwdV;
+__global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p, int64_t run, int64_t runs) {
+  constexpr int V = kV;
   using VT = VecOf<T, V>;
   const int64_t nv = p.D / V;
-  const int64_t id = int64_t(blockIdx.x) * kBwdThreads + threadIdx.x;
+  const int64_t id = int64_t(blockIdx.x) * kRunThreads + threadIdx.x;
   const int64_t br = id / nv, d0 = (id - br * nv) * V, b = br / runs;
   if (b >= p.B) return;
   const int64_t t0 = (br - b * runs) * run, t1 = min64(t0 + run, p.T);
@@ -289,18 +318,18 @@ constexpr int64_t kFwdWant = 148 * 1024, kBwdWant = 148 * 512;
 
 template <typename T, int W, bool SILU>
 cudaError_t fwd(const ConvArgs& p, cudaStream_t s) {
-  const int64_t nv = p.D / Vec16<T>::n, run = run_length(p.B, p.T, nv, 32, kFwdWant), runs = (p.T + run - 1) / run;
-  const int64_t blocks = (p.B * runs * nv + kThreads - 1) / kThreads;
+  const int64_t nv = p.D / kV, run = run_length(p.B, p.T, nv, 32, kFwdWant), runs = (p.T + run - 1) / run;
+  const int64_t blocks = (p.B * runs * nv + kRunThreads - 1) / kRunThreads;
   if (blocks > 2147483647) return cudaErrorInvalidValue;
-  conv_fwd_kernel<T, W, SILU><<<unsigned(blocks), kThreads, 0, s>>>(p, run, runs);
+  conv_fwd_kernel<T, W, SILU><<<unsigned(blocks), kRunThreads, 0, s>>>(p, run, runs);
   return cudaGetLastError();
 }
 template <typename T, int W, bool SILU>
 cudaError_t bwd(const ConvArgs& p, cudaStream_t s) {
-  const int64_t nv = p.D / kBwdV, run = run_length(p.B, p.T, nv, 64, kBwdWant), runs = (p.T + run - 1) / run;
-  const int64_t blocks = (p.B * runs * nv + kBwdThreads - 1) / kBwdThreads;
+  const int64_t nv = p.D / kV, run = run_length(p.B, p.T, nv, 64, kBwdWant), runs = (p.T + run - 1) / run;
+  const int64_t blocks = (p.B * runs * nv + kRunThreads - 1) / kRunThreads;
   if (blocks > 2147483647) return cudaErrorInvalidValue;
-  conv_bwd_kernel<T, W, SILU><<<unsigned(blocks), kBwdThreads, 0, s>>>(p, run, runs);
+  conv_bwd_kernel<T, W, SILU><<<unsigned(blocks), kRunThreads, 0, s>>>(p, run, runs);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.scratch) return e;
   conv_dw_kernel<<<unsigned(((W + 1) * p.D + 31) / 32), 1024, 0, s>>>(p, p.B * runs);
@@ -341,7 +370,7 @@ cudaError_t run(Kind k, const ConvArgs& p, int dtype, cudaStream_t s) {
 
 int64_t conv_scratch_floats(int64_t B, int64_t T, int64_t D, int W) {
   if (B == 0 || T == 0 || D == 0) return 0;
-  const int64_t run = run_length(B, T, D / kBwdV, 64, kBwdWant);
+  const int64_t run = run_length(B, T, D / kV, 64, kBwdWant);
   return B * ((T + run - 1) / run) * (W + 1) * D;
 }
 

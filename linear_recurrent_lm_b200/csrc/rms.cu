@@ -31,35 +31,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ float scale_of(float top) { return top == 0.f ? 1.f : max_nan(top * (1.f / kE4m3Max), kMinScale); }
 
-// Sum over the TPS threads of a slice of two values at once.  All threads of the CTA call it together.
+// Sums (or, of the first, the maximum) over the TPS threads of a slice of COUNT = 1 or 2 values at once.  All threads
+// of the CTA call it together.
 struct Pair { float a, b; };
-template <bool MAXA>
+template <bool MAXA, int COUNT>
 __device__ __forceinline__ Pair slice_reduce(Pair v, int tps, float (*sm)[2]) {
-  const int w = tps < 32 ? tps : 32;
-  for (int o = w / 2; o; o >>= 1) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    if (o >= tps) continue;
     const float a = __shfl_xor_sync(0xffffffffu, v.a, o);
     v.a = MAXA ? max_nan(v.a, a) : v.a + a;
-    v.b += __shfl_xor_sync(0xffffffffu, v.b, o);
+    if (COUNT == 2) v.b += __shfl_xor_sync(0xffffffffu, v.b, o);
   }
   if (tps <= 32) return v;
   const int warp = threadIdx.x >> 5, nw = tps >> 5, first = warp & ~(nw - 1);
   __syncthreads();   // the last use of `sm` is over
-  if ((threadIdx.x & 31) == 0) {
-    sm[warp][0] = v.a;
-    sm[warp][1] = v.b;
-  }
+  if ((threadIdx.x & 31) == 0) *reinterpret_cast<float2*>(sm[warp]) = make_float2(v.a, v.b);
   __syncthreads();
-  Pair r{sm[first][0], sm[first][1]};
+  float2 r = *reinterpret_cast<const float2*>(sm[first]);
   for (int i = 1; i < nw; ++i) {
-    r.a = MAXA ? max_nan(r.a, sm[first + i][0]) : r.a + sm[first + i][0];
-    r.b += sm[first + i][1];
+    const float2 q = *reinterpret_cast<const float2*>(sm[first + i]);
+    r.x = MAXA ? max_nan(r.x, q.x) : r.x + q.x;
+    if (COUNT == 2) r.y += q.y;
   }
-  return r;
+  return Pair{r.x, r.y};
 }
 
 struct Shape {
   int64_t L, slices;   // channels of a slice; rows * groups
-  int tps, spc;        // threads per slice, slices per CTA
+  int tps, spc;        // threads per slice (a power of two), slices per CTA
+  int log_tps;
+  float inv_l;         // 1 / L
 };
 
 template <typename T, int V>
@@ -79,18 +81,18 @@ template <typename T, int VPT, int MODE, int QUANT>   // QUANT: 0 none, 1 per 12
 __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const RmsArgs p, const Shape s) {
   constexpr int V = Vec16<T>::n;
   using VT = VecOf<T, V>;
-  __shared__ float sm[32][2];
-  const int lane = threadIdx.x % s.tps, sub = threadIdx.x / s.tps;
+  __shared__ __align__(8) float sm[32][2];
+  const int lane = threadIdx.x & (s.tps - 1), sub = threadIdx.x >> s.log_tps;
   const int64_t nv = s.L / V, total = p.rows * p.D;
   for (int64_t s0 = int64_t(blockIdx.x) * s.spc; s0 < s.slices; s0 += int64_t(gridDim.x) * s.spc) {
     const int64_t slice = s0 + sub;
-    const int64_t row = slice / p.groups, g = slice - row * p.groups;
+    const int64_t row = p.groups == 1 ? slice : slice / p.groups, g = p.groups == 1 ? 0 : slice - row * p.groups;
     const int64_t base = row * p.D + g * s.L;
     typename VT::R rx[VPT], rz[VPT];
     bool act[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = int64_t(i) * s.tps + lane;
+      const int64_t v = i * s.tps + lane;
       act[i] = slice < s.slices && v < nv && range_ok(base + v * V, V, total, p.status);
       if (act[i]) {
         rx[i] = VT::load(static_cast<const T*>(p.x) + base + v * V);
@@ -108,8 +110,12 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const R
           VT::get(rz[i], z);
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            // the stored sum is normalised, so that the backward, which reads it, sees the same h
-            h[i][e] = MODE == kResidual ? Elt<T>::to_f32(Elt<T>::from_f32(h[i][e] + z[e])) : h[i][e] * (z[e] * sigmoid_of<T>(z[e]));
+            h[i][e] = MODE == kResidual ? h[i][e] + z[e] : h[i][e] * (z[e] * sigmoid_of<T>(z[e]));
+          if (MODE == kResidual) {   // the stored sum is normalised, so that the backward, which reads it, sees the same h
+            rx[i] = VT::pack(h[i]);
+            VT::get(rx[i], h[i]);
+            VT::put(static_cast<T*>(p.h_out) + base + (i * s.tps + lane) * V, rx[i]);
+          }
         }
       } else {
 #pragma unroll
@@ -118,15 +124,11 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const R
 #pragma unroll
       for (int e = 0; e < V; ++e) ss = fmaf(h[i][e], h[i][e], ss);
     }
-    const float rstd = rsqrtf(slice_reduce<false>(Pair{ss, 0.f}, s.tps, sm).a / float(s.L) + p.eps);
-    if (MODE == kResidual)
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (act[i]) VT::store(static_cast<T*>(p.h_out) + base + (int64_t(i) * s.tps + lane) * V, h[i]);
+    const float rstd = rsqrtf(fmaf(slice_reduce<false, 1>(Pair{ss, 0.f}, s.tps, sm).a, s.inv_l, p.eps));
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = int64_t(i) * s.tps + lane;
+      const int64_t v = i * s.tps + lane;
       if (act[i]) {
         const float4* w = reinterpret_cast<const float4*>(p.weight + g * s.L + v * V);
 #pragma unroll
@@ -145,29 +147,29 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const R
 #pragma unroll
           for (int o = 64 / V; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
           const float sc = scale_of(m);
-          const float inv = 1.f / sc;
+          const float inv = rcp_fast(sc);   // sc >= 2^-100, or NaN
           if (act[i]) {
             float q[V];
 #pragma unroll
             for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
             store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + v * V, q);
-            if (v % (128 / V) == 0) p.scale[(base + v * V) / 128] = sc;
+            if ((lane & (128 / V - 1)) == 0) p.scale[(base + v * V) >> 7] = sc;
           }
         }
         top = max_nan(top, m);
       }
     }
     if (QUANT == 2) {
-      top = slice_reduce<true>(Pair{top, 0.f}, s.tps, sm).a;
+      top = slice_reduce<true, 1>(Pair{top, 0.f}, s.tps, sm).a;
       const float sc = scale_of(top);
-      const float inv = 1.f / sc;
+      const float inv = rcp_fast(sc);
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
         if (act[i]) {
           float q[V];
 #pragma unroll
           for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
-          store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + (int64_t(i) * s.tps + lane) * V, q);
+          store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + (i * s.tps + lane) * V, q);
         }
       if (lane == 0 && slice < s.slices) p.scale[slice] = sc;
     }
@@ -177,19 +179,19 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const R
 // Backward.  A CTA stays on one group of channels (blockIdx.x % groups), so a thread keeps its channels' dweight
 // in registers over all its rows; the CTA's sum goes to its row of scratch, and column_sums adds those rows.
 template <typename T, int VPT, bool GATE>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta, VPT == 4 ? 1 : 3) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
   constexpr int V = Vec16<T>::n;
   using VT = VecOf<T, V>;
-  __shared__ float sm[32][2];
+  __shared__ __align__(8) float sm[32][2];
   extern __shared__ float acc[];   // [spc][L] when a CTA holds several slices
-  const int lane = threadIdx.x % s.tps, sub = threadIdx.x / s.tps;
+  const int lane = threadIdx.x & (s.tps - 1), sub = threadIdx.x >> s.log_tps;
   const int64_t nv = s.L / V, total = p.rows * p.D;
   const int64_t g = blockIdx.x % p.groups, blk = blockIdx.x / p.groups;
   float dw[VPT][V] = {};
   float wt[VPT][V];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int64_t v = int64_t(i) * s.tps + lane;
+    const int64_t v = i * s.tps + lane;
 #pragma unroll
     for (int e = 0; e < V; ++e) wt[i][e] = v < nv ? __ldg(p.weight + g * s.L + v * V + e) : 0.f;
   }
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const R
     bool act[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = int64_t(i) * s.tps + lane, o = base + v * V;
+      const int64_t v = i * s.tps + lane, o = base + v * V;
       act[i] = row < p.rows && v < nv && range_ok(o, V, total, p.status);
       if (act[i]) {
         rx[i] = VT::load(static_cast<const T*>(p.x) + o);
@@ -224,13 +226,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const R
           gh = fmaf(d[e] * wt[i][e], h, gh);
         }
       }
-    const Pair r = slice_reduce<false>(Pair{ss, gh}, s.tps, sm);
-    const float rstd = rsqrtf(r.a / float(s.L) + p.eps);
-    const float m = r.b * rstd * rstd / float(s.L);   // mean(g xhat) rstd: dh = rstd (g - h m)
+    const Pair r = slice_reduce<false, 2>(Pair{ss, gh}, s.tps, sm);
+    const float rstd = rsqrtf(fmaf(r.a, s.inv_l, p.eps));
+    const float m = r.b * rstd * rstd * s.inv_l;   // mean(g xhat) rstd: dh = rstd (g - h m)
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (act[i]) {
-        const int64_t o = base + (int64_t(i) * s.tps + lane) * V;
+        const int64_t o = base + (i * s.tps + lane) * V;
         float x[V], z[V], d[V], dx[V], dz[V];
         VT::get(rx[i], x);
         VT::get(rg[i], d);
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const R
   if (s.spc == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = int64_t(i) * s.tps + lane;
+      const int64_t v = i * s.tps + lane;
       if (v < nv)
 #pragma unroll
         for (int u = 0; u < V / 4; ++u)
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_bwd_kernel(const R
   }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int64_t v = int64_t(i) * s.tps + lane;
+    const int64_t v = i * s.tps + lane;
     if (v < nv)
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[sub * s.L + v * V + e] = dw[i][e];
@@ -292,7 +294,12 @@ Shape shape_of(const RmsArgs& p, int64_t nv, int vpt) {
   s.L = p.D / p.groups;
   s.slices = p.rows * p.groups;
   s.tps = 1;
-  while (int64_t(s.tps) * vpt < nv) s.tps *= 2;
+  s.log_tps = 0;
+  while (int64_t(s.tps) * vpt < nv) {
+    s.tps *= 2;
+    ++s.log_tps;
+  }
+  s.inv_l = 1.f / float(s.L);
   s.spc = s.tps < kCta ? kCta / s.tps : 1;
   return s;
 }

@@ -154,6 +154,7 @@ SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool c
     }
   } else {
     s.dstate = take(2 * B * H * nc * state);
+    s.seg = take(2 * ssm_run_floats(B, T, H, N));
     s.state_t = take(2 * B * H * (nc + 1) * state);
     s.dcp = take(2 * B * T * H * N);
     s.dbp = take(2 * B * T * H * N);

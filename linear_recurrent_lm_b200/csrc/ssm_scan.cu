@@ -38,6 +38,11 @@ struct ScanOp {
                                          // scans: fp64): [B,H,stride], or null
   int64_t chunk_stride;
   float* last;                           // [B,H,R,K]: Z after the walk (reverse: carried through token 0's decay), or null
+  // The walk may be cut into `segments` runs of `per` tokens: a first pass (`local`) leaves each run's end state from
+  // zero and its total decay, and the second starts every run from what those before it left.
+  int64_t segments, per;
+  bool local;
+  void *seg_state, *seg_decay;           // [B,H,segments] states [R][K] and decays, fp32 (transposed scans: fp64)
 };
 
 // 16 bytes of staged values.
@@ -77,7 +82,7 @@ __device__ __forceinline__ void advance(double* z0, double* z1, const double (&k
 }
 
 // TR: the transposed scans (R = N, K = 64), in double.
-template <typename T, int R, int K, bool REV, bool TR>
+template <typename T, int R, int K, bool REV, bool TR, bool LOCAL>
 __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const ScanOp op) {
   using F = typename std::conditional<TR, double, float>::type;
   using F2 = typename std::conditional<TR, double2, float2>::type;
@@ -88,8 +93,8 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
   __shared__ F s_f[2][kTile], s_i[2][kTile], s_o[2][kTile];
   __shared__ __align__(16) F s_out[kTile][R];
   const int tid = threadIdx.x, lane8 = tid & 7, r0 = (tid >> 3) * 2;
-  const int64_t unit = blockIdx.x, b = unit / p.H, h = unit - b * p.H, g = h / (p.H / p.G);
-  const int64_t T_ = p.T;
+  const int64_t unit = blockIdx.x / op.segments, seg = blockIdx.x - unit * op.segments, b = unit / p.H, h = unit - b * p.H, g = h / (p.H / p.G);
+  const int64_t T_ = p.T, first = seg * op.per, end = min64(first + op.per, T_);   // positions of the walk
   const float A = __ldg(p.A + h);
   const float skip = op.skip ? __ldg(op.skip + h) : 0.f;
 
@@ -101,8 +106,20 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
         const int row = r0 + i, col = (8 * u + lane8) * EV + e;   // init is [64][N]: transposed where R = N
-        Z[i][EV * u + e] = op.init ? F(__ldg(op.init + unit * R * K + (TR ? col * R + row : row * K + col))) : F(0);
+        Z[i][EV * u + e] = !LOCAL && op.init ? F(__ldg(op.init + unit * R * K + (TR ? col * R + row : row * K + col))) : F(0);
       }
+  if (!LOCAL)
+    for (int64_t j = unit * op.segments; j < unit * op.segments + seg; ++j) {
+      const F f = static_cast<const F*>(op.seg_decay)[j];
+      const F* z = static_cast<const F*>(op.seg_state) + j * (R * K);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < NI; ++u)
+#pragma unroll
+          for (int e = 0; e < EV; ++e) Z[i][EV * u + e] = f * Z[i][EV * u + e] + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
+    }
+  F total = 1;
   auto put_state = [&](auto* dst, F f) {
     using D = std::remove_pointer_t<decltype(dst)>;
     using D2 = typename std::conditional<sizeof(D) == 8, double2, float2>::type;
@@ -127,7 +144,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
       raw[q] = make_uint4(0, 0, 0, 0);
       if (v < kVecs) {
         const int tok = v / (VR + 2 * VK), o = v % (VR + 2 * VK);
-        if (pos0 + tok < T_) {
+        if (pos0 + tok < end) {
           const int64_t bt = b * T_ + token(pos0 + tok);
           const int which = o < VR ? 0 : o < VR + VK ? 1 : 2;
           const int j = o - (which == 0 ? 0 : which == 1 ? VR : VR + VK), width = which == 0 ? R : K;
@@ -138,7 +155,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
         }
       }
     }
-    if (tid < kTile && pos0 + tid < T_) {
+    if (tid < kTile && pos0 + tid < end) {
       const int64_t t = token(pos0 + tid), bt = b * T_ + t;
       const float d = step_of<T>(p, bt, h);
       const int64_t td = REV ? t + 1 : t;   // the decay between this token and the one walked before it
@@ -169,30 +186,32 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
     }
   };
 
-  fetch(0);
+  fetch(first);
   stage(0);
   __syncthreads();
   int buf = 0;
-  for (int64_t pos0 = 0; pos0 < T_; pos0 += kTile, buf ^= 1) {
-    const int n = int(min64(kTile, T_ - pos0));
-    if (pos0 + kTile < T_) fetch(pos0 + kTile);
+  for (int64_t pos0 = first; pos0 < end; pos0 += kTile, buf ^= 1) {
+    const int n = int(min64(kTile, end - pos0));
+    if (pos0 + kTile < end) fetch(pos0 + kTile);
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const F f = s_f[buf][i];
       const int64_t t = token(pos0 + i);
-      if (op.chunk_state && (REV ? (t % kSsmChunk == kSsmChunk - 1 || t == T_ - 1) : t % kSsmChunk == 0))
+      if (!LOCAL && op.chunk_state && (REV ? (t % kSsmChunk == kSsmChunk - 1 || t == T_ - 1) : t % kSsmChunk == 0))
         put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + t / kSsmChunk) * (R * K), REV ? f : F(1));
       const F in = s_i[buf][i];
       const F2 rv = *reinterpret_cast<const F2*>(&s_r[buf][i][r0]);
       const F u0 = in * rv.x, u1 = in * rv.y;
+      if (LOCAL) total *= f;
       F2 a0{}, a1{}, own{};
 #pragma unroll
       for (int u = 0; u < NI; ++u) {
         F k[EV], c[EV];
         load_pair(&s_k[buf][i][(8 * u + lane8) * EV], k);
         load_pair(&s_c[buf][i][(8 * u + lane8) * EV], c);
-        advance(&Z[0][EV * u], &Z[1][EV * u], k, c, f, u0, u1, a0, a1, own);
+        advance(&Z[0][EV * u], &Z[1][EV * u], k, c, f, u0, u1, a0, a1, own);   // (LOCAL: the outputs fall away)
       }
+      if (LOCAL) continue;
       F o0 = a0.x + a0.y, o1 = a1.x + a1.y, kc = own.x + own.y;
 #pragma unroll
       for (int o = 1; o < 8; o *= 2) {
@@ -209,8 +228,9 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
         *reinterpret_cast<F2*>(&s_out[i][r0]) = F2{o0, o1};
       }
     }
-    if (pos0 + kTile < T_) stage(buf ^ 1);
+    if (pos0 + kTile < end) stage(buf ^ 1);
     __syncthreads();
+    if constexpr (LOCAL) continue;
     if constexpr (TR) {
       for (int v = tid; v < n * (R / 2); v += NT) {
         const int i = v / (R / 2), j = v % (R / 2);
@@ -230,6 +250,12 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
     }
     __syncthreads();
   }
+  if (LOCAL) {
+    put_state(static_cast<F*>(op.seg_state) + blockIdx.x * int64_t(R * K), F(1));
+    if (tid == 0) static_cast<F*>(op.seg_decay)[blockIdx.x] = total;
+    return;
+  }
+  if (seg != op.segments - 1) return;
   if (op.last) {
     F f = 1;
     if (REV && T_ > 0) f = (p.reset && p.reset[b * T_]) ? F(0) : decay(step_of<T>(p, b * T_, h));
@@ -238,9 +264,27 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
   if (!REV && op.chunk_state) put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + chunks_of(T_)) * (R * K), F(1));
 }
 
+// Runs of a row's tokens: with fewer rows of heads than two per SM, as many as fill those slots, of at least 32 tokens.  A
+// cut row is walked twice, so it takes three runs to gain (B=2 T=512 H=12 N=64 fp32, forward: 140 us whole).
+int64_t scan_segments(int64_t units, int64_t T) {
+  const int64_t fit = units > 0 ? 296 / units : 1, most = T / 32, k = fit < most ? fit : most;
+  return k >= 3 ? k : 1;
+}
+
 template <typename T, int R, int K, bool REV, bool TR>
-cudaError_t scan(const SsmArgs& p, const ScanOp& op, cudaStream_t s) {
-  scan_kernel<T, R, K, REV, TR><<<unsigned(p.B * p.H), 4 * R, 0, s>>>(p, op);
+cudaError_t scan(const SsmArgs& p, ScanOp op, float* seg, cudaStream_t s) {
+  const int64_t units = p.B * p.H, k = seg ? scan_segments(units, p.T) : 1;
+  op.per = (p.T + k - 1) / k;
+  op.segments = op.per > 0 ? (p.T + op.per - 1) / op.per : 1;
+  if (op.segments > 1) {
+    using F = typename std::conditional<TR, double, float>::type;
+    op.seg_state = seg;
+    op.seg_decay = reinterpret_cast<F*>(seg) + units * op.segments * R * K;
+    scan_kernel<T, R, K, REV, TR, true><<<unsigned(units * op.segments), 4 * R, 0, s>>>(p, op);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  scan_kernel<T, R, K, REV, TR, false><<<unsigned(units * op.segments), 4 * R, 0, s>>>(p, op);
   return cudaGetLastError();
 }
 
@@ -257,7 +301,7 @@ cudaError_t fwd(const SsmArgs& p, cudaStream_t s) {
   op.chunk_state = p.ckpt;
   op.chunk_stride = chunks_of(p.T) + 1;
   op.last = p.s_out;
-  return scan<T, kHeadP, N, false, false>(p, op, s);
+  return scan<T, kHeadP, N, false, false>(p, op, p.ckpt ? p.ckpt + p.B * p.H * (chunks_of(p.T) + 1) * kHeadP * N : nullptr, s);
 }
 
 // Sums over the heads of a group: with the scans' past parts Pc, Pb per head and q = x . dy,
@@ -344,6 +388,7 @@ template <typename T, int N>
 cudaError_t bwd(const SsmArgs& p, cudaStream_t s) {
   const SsmScratch sc = ssm_scratch(p.B, p.T, p.H, p.G, N, false);
   const int64_t nc = chunks_of(p.T);
+  float* seg = p.scratch + sc.seg;
   ScanOp dc{};   // forward again, transposed
   dc.rin = p.b; dc.rin_ld = p.b_ld; dc.rin_g = true;
   dc.kin = p.x; dc.kin_ld = p.x_ld;
@@ -369,9 +414,9 @@ cudaError_t bwd(const SsmArgs& p, cudaStream_t s) {
   db.out = p.scratch + sc.dbp;
   db.chunk_state = p.scratch + sc.dstate; db.chunk_stride = nc;
   cudaError_t e;
-  if ((e = scan<T, N, kHeadP, false, true>(p, dc, s)) != cudaSuccess) return e;
-  if ((e = scan<T, kHeadP, N, true, false>(p, dx, s)) != cudaSuccess) return e;
-  if ((e = scan<T, N, kHeadP, true, true>(p, db, s)) != cudaSuccess) return e;
+  if ((e = scan<T, N, kHeadP, false, true>(p, dc, seg, s)) != cudaSuccess) return e;
+  if ((e = scan<T, kHeadP, N, true, false>(p, dx, seg, s)) != cudaSuccess) return e;
+  if ((e = scan<T, N, kHeadP, true, true>(p, db, seg, s)) != cudaSuccess) return e;
   heads_kernel<T, N><<<unsigned((p.B * p.T * p.G + 7) / 8), 256, 0, s>>>(p, sc);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   anchor_kernel<<<unsigned(p.B * p.H * nc), 256, 0, s>>>(p, sc);
@@ -393,6 +438,12 @@ cudaError_t run_dtype(const SsmArgs& p, int dtype, bool backward, cudaStream_t s
 }
 
 }  // namespace
+
+// fp32 elements of the runs' states and decays (fp64: twice as many).
+int64_t ssm_run_floats(int64_t B, int64_t T, int64_t H, int N) {
+  const int64_t k = scan_segments(B * H, T);
+  return k > 1 ? B * H * k * (kHeadP * N + 1) : 0;
+}
 
 cudaError_t launch_ssm_scan_fwd(const SsmArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, false, s); }
 cudaError_t launch_ssm_scan_bwd(const SsmArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, true, s); }

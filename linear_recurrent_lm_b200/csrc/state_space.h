@@ -89,13 +89,15 @@ struct SsmScratch {
   int64_t dstate;          // [B,H,nc] gradient of the state after each chunk (SCAN: d, transposed)
   int64_t state_t;         // SCAN: d [B,H,nc+1] states before each chunk and the last, transposed as dstate
   int64_t dcp, dbp;        // SCAN: d [B,T,H,N] the past's part of dc and db per head
-  int64_t seg;             // CHUNKED: end states and decays of the segments of a cut row (see ssm_chunk.cu)
+  int64_t seg;             // end states and decays of the segments of a cut row
   int64_t db_part, dc_part;   // CHUNKED: [splits][B,T,G,N] sums over the heads of a split, where there are several
   int64_t splits;             // CHUNKED: parts that a group's heads are cut into
   int64_t total;
 };
 SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool chunked);
-int64_t ssm_segment_floats(int64_t B, int64_t T, int64_t H, int N);   // of the part `seg`, forward and backward alike
+// fp32 elements of the part `seg` (the forward's is behind its checkpoints): CHUNKED; SCAN (twice that in the backward).
+int64_t ssm_segment_floats(int64_t B, int64_t T, int64_t H, int N);
+int64_t ssm_run_floats(int64_t B, int64_t T, int64_t H, int N);
 
 cudaError_t launch_ssm_scan_fwd(const SsmArgs& p, int dtype, cudaStream_t s);
 cudaError_t launch_ssm_scan_bwd(const SsmArgs& p, int dtype, cudaStream_t s);

@@ -215,7 +215,7 @@ size_t wkv7_ssm_workspace_bytes(const wkv7_desc_t* d, const wkv7_ssm_t* sp) {
   wkv7::SsmArgs a;
   if (check_ssm(d, sp, &a, true) != WKV7_OK || d->T == 0) return 0;
   const int64_t nc = (d->T + wkv7::kSsmChunk - 1) / wkv7::kSsmChunk;
-  return size_t(d->B * d->H * (nc + 1) * wkv7::kHeadP * d->N + (chunked(d) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : 0)) * 4;
+  return size_t(d->B * d->H * (nc + 1) * wkv7::kHeadP * d->N + (chunked(d) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : wkv7::ssm_run_floats(d->B, d->T, d->H, d->N))) * 4;
 }
 
 wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const void* x, const void* dt, const void* b,

@@ -492,7 +492,7 @@ def _mask(t: Optional[torch.Tensor], name: str, shape, like: torch.Tensor):
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor):
     if t is None:
-        return torch.empty(shape, device=like.device, dtype=dtype)
+        return like.new_empty(shape) if dtype == like.dtype else like.new_empty(shape, dtype=dtype)
     _dense(t, name, shape, dtype, like)
     return t
 
@@ -502,7 +502,7 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _scratch(n: int, like: torch.Tensor):
-    return torch.empty(max(n, 16), device=like.device, dtype=torch.uint8)
+    return like.new_empty(max(n, 16), dtype=torch.uint8)
 
 
 def _now(like: torch.Tensor):

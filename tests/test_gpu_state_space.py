@@ -270,7 +270,15 @@ def test_ssm_split_equals_one_call(W, dtype, algo):
     ds, _ = _dev(rng.standard_normal((2, 4, 64, 64)).astype(np.float32))
     y, s, ws = W.ssm_forward(**dev, algo=algo)
     g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo=algo, **dev)
-    same = _near if algo == "chunked" else lambda a, b, n: _close(a, _f64(b), dtype, FP32, n)
+    def same(a, b, n):   # both are stored: each is off by up to half a step, so they may differ by a whole one
+        if algo == "chunked":
+            return _near(a, b, n)
+        if dtype == "f32":
+            return _close(a, _f64(b), dtype, FP32, n)
+        b = _f64(b)
+        step = 2.0 * np.maximum(np.abs(b), np.abs(_f64(a))) * 2.0 ** (-8 if dtype == "bf16" else -11)
+        worst = np.max(np.maximum(np.abs(_f64(a) - b) - step, 0.0)) / np.sqrt(np.mean(b * b))
+        assert worst <= FP32, (n, worst)
     for cut in (128, 77):
         part = lambda a, z: {n: (v[:, a:z].contiguous() if n in ("x", "dt", "b", "c", "reset") else v) for n, v in dev.items()}   # noqa: E731
         first, second = part(0, cut), part(cut, 290)
