@@ -304,7 +304,7 @@ Shape shape_of(const RmsArgs& p, int64_t nv, int vpt) {
   return s;
 }
 constexpr int64_t kFwdCtas = 148 * 16;   // grid-stride over the rest
-constexpr int64_t kBwdThreads = 148 * 1024;   // resident threads of the backward at its 64-odd registers
+constexpr int64_t kBwdThreads = 148 * 768;   // resident threads of the backward at its 80 registers: one wave
 
 // CTAs per group of the backward: its scratch rows.
 int64_t bwd_blocks(int64_t rows, int64_t groups, int tps, int spc) {

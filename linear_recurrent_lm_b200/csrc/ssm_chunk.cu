@@ -41,7 +41,9 @@ template <int N, bool OUT>
 struct Smem {
   static constexpr int kNB = N / 64;             // 64-column tiles of b and c
   static constexpr int kX = 0, kB = kX + 2 * kTileBytes, kC = kB + 2 * kNB * kTileBytes;
-  static constexpr int kXS = kC + (OUT ? kNB * kTileBytes : 0), kSH = kXS + 3 * kTileBytes;
+  // the parts of the weighted x twice where they fit: then those of the next chunk are made while this one's product runs
+  static constexpr int kXSets = OUT && N == 128 ? 1 : 2;
+  static constexpr int kXS = kC + (OUT ? kNB * kTileBytes : 0), kSH = kXS + kXSets * 3 * kTileBytes;
   static constexpr int kEnd = kSH + (OUT ? 2 * N * 128 : 0);
   struct Tail {
     Decays dec[3];
@@ -55,7 +57,7 @@ struct Smem {
   static constexpr int kBytes = kEnd + int(sizeof(Tail)) + 1024;
 };
 // TMEM columns
-constexpr uint32_t kTG = 0, kTM = 128, kTY1 = 192, kTY2 = 256, kTU = 384;
+constexpr uint32_t kTG = 0, kTM = 128, kTY1 = 192, kTY2 = 256, kTU = 384;   // kTY2, kTU: two of 64 each
 
 template <int N, bool OUT, bool REV>
 __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p, const __grid_constant__ TileMaps tm, const ChunkOp op) {
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         products(tmem + kTY2 + 64 * (e & 1), dC, 32, kTileBytes, NB, dSH, 2048, 8192, 2 * NB, kIdY, &tl.y2_done);
       }
       if (!(ok = wait.warp(&tl.xs_ready[e & 1], ph(e)))) break;       // U(e) = B^T (w X), transposed state [N][64]: three parts
-      products(tmem + kTU, dBm + bt, 2048, 8192, 2, dXS, 2048, 8192, 6, kIdU, &tl.u_full[e & 1]);
+      products(tmem + kTU + 64 * (e & 1), dBm + bt, 2048, 8192, 2, dXS + (e % SM::kXSets * 3 * kTileBytes >> 4), 2048, 8192, 6, kIdU,
+               &tl.u_full[e & 1]);
     }
   } else {
     // ------------------------------------------------------------ the working warps
@@ -220,10 +223,42 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
 #pragma unroll
         for (int q = 0; q < 16; ++q) dst[at + q * N] = S[q];
     };
-    float total = 1.f;
-    bool ok = true;
+    // The weighted x of chunk e in three bf16 parts (its buffer has been read).  The smallest part first: the tensor core
+    // cuts its sums off below their leading bits, which the large part then meets in its own eight steps only.
+    auto weigh = [&](int e) {
+      if (!wait.warp(&tl.dec_full[e % 3], ph3(e)) || !wait.warp(&tl.x_full[e & 1], ph(e))) return false;
+      const Decays& nd = tl.dec[e % 3];
+      const float wt = REV ? nd.in[row] : nd.d[row] * nd.out[row];
+      uint8_t* xs = sm + SM::kXS + e % SM::kXSets * 3 * kTileBytes;
 #pragma unroll 1
-    for (int i = -1; i < n; ++i) {
+      for (int j = 2 * r; j < 2 * r + 2; ++j) {
+        const uint32_t o = swz(row, j);
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + SM::kX + (e & 1) * kTileBytes + o);
+        const uint32_t xi[4] = {v.x, v.y, v.z, v.w};
+        uint32_t part[3][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float2 f = mul2(stc::unpack(xi[k]), make_float2(wt, wt));
+          part[0][k] = split(f);
+          part[1][k] = split(f);
+          part[2][k] = pack(f.x, f.y);
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<uint4*>(xs + (2 - q) * kTileBytes + o) = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
+      }
+      tc::fence_smem_to_async();
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&tl.xs_ready[e & 1]);
+        if (!OUT) arrive(&tl.x_free[e & 1]);
+      }
+      return true;
+    };
+    float total = 1.f;
+    bool ok = SM::kXSets == 1 || weigh(0);
+#pragma unroll 1
+    for (int i = -1; ok && i < n; ++i) {
       const Decays& dec = tl.dec[(i + 3) % 3];
       float in = 0.f;
       if (i >= 0) {
@@ -254,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
                 for (int e = 0; e < 4; ++e) {
                   const float gd = v[s + e] * ds[e];
                   own = c + s + e <= row ? gd : own;   // the last one is M_tt, if it is in these columns
-                  v[s + e] = c + s + e < row ? gd * ex2((hi - hs[e]) + (lo - ls[e])) : 0.f;
+                  const float x = (hi - hs[e]) + (lo - ls[e]);   // (the exponent is masked, not the result: no branch)
+                  v[s + e] = gd * ex2(c + s + e < row ? x : -1e30f);
                 }
               }
               if ((row & 127) >> 4 == c >> 4) tl.own[i & 1][row] = own;
@@ -285,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           __syncwarp();
           if (lane == 0) arrive(&tl.m_ready[i & 1]);
         }
+        if (SM::kXSets == 2 && i + 1 < n && !(ok = weigh(i + 1))) break;   // (U(i - 1) has read that buffer)
         // ---- S(i + 1) = e^{Lambda_end} S(i) + U(i)
         const float gam = dec.total;
         total *= gam;
@@ -293,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         if (!(ok = wait.warp(&tl.u_full[i & 1], ph(i)))) break;
         tc::fence_after_sync();
         float u[16];
-        ld16(lanes + kTU + 16 * r, u);
+        ld16(lanes + kTU + 64 * (i & 1) + 16 * r, u);
         tc::wait_ld();
         tc::fence_before_sync();
 #pragma unroll
@@ -322,34 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           if (lane == 0) arrive(&tl.sh_ready[e & 1]);
         }
         if (op.states) put(op.states + (unit * op.stride + chunk(e)) * 64 * N);
-        // ---- XS(e) (U(i) has read its parts).  The smallest part first: the tensor core cuts its sums off below their
-        // leading bits, which the large part then meets in its own eight steps only
-        if (!(ok = wait.warp(&tl.dec_full[e % 3], ph3(e)) && wait.warp(&tl.x_full[e & 1], ph(e)))) break;
-        const Decays& nd = tl.dec[e % 3];
-        const float wt = REV ? nd.in[row] : nd.d[row] * nd.out[row];
-#pragma unroll 1
-        for (int j = 2 * r; j < 2 * r + 2; ++j) {
-          const uint32_t o = swz(row, j);
-          const uint4 v = *reinterpret_cast<const uint4*>(sm + SM::kX + (e & 1) * kTileBytes + o);
-          const uint32_t xi[4] = {v.x, v.y, v.z, v.w};
-          uint32_t part[3][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float2 f = mul2(stc::unpack(xi[k]), make_float2(wt, wt));
-            part[0][k] = split(f);
-            part[1][k] = split(f);
-            part[2][k] = pack(f.x, f.y);
-          }
-#pragma unroll
-          for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<uint4*>(sm + SM::kXS + (2 - q) * kTileBytes + o) = make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
-        }
-        tc::fence_smem_to_async();
-        __syncwarp();
-        if (lane == 0) {
-          arrive(&tl.xs_ready[e & 1]);
-          if (!OUT) arrive(&tl.x_free[e & 1]);
-        }
+        if (SM::kXSets == 1 && !(ok = weigh(e))) break;   // (U(i) has read its parts)
       }
       if (OUT && i >= 0) {
         // ---- Y(i) = Y1 + in Y2 + (D + M_tt) x

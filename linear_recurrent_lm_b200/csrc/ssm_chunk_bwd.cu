@@ -44,7 +44,7 @@ struct Smem {
     float rp[4][kQ], fp[4][kQ];
     float own_g[kQ], own_k[kQ];
     double sds[kWorkers];
-    unsigned long long bc_full, xy_full, xy_free, gk_full, s_ready, w_ready, y2_full, m_done, ds_ready, e_full, ab_free, quad[4],
+    unsigned long long bc_full, xy_full, xy_free, gk_full, s_ready, w_ready, y2_full, m_done, ds_ready, xi_full, e_full, ab_free, quad[4],
         dec_full[3], dec_free[3], drained;
     uint32_t tmem;
     int dead;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
 
   if (threadIdx.x == 0) {
     tl.dead = 0;
-    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.e_full, &tl.drained};
+    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full, &tl.drained};
     for (auto* bar : one) mbar_init(bar, 1);
     unsigned long long* all[] = {&tl.xy_free, &tl.s_ready, &tl.w_ready, &tl.ds_ready, &tl.ab_free};
     for (auto* bar : all) mbar_init(bar, kWorkers);
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       tc::fence_after_sync();
       if (elected()) {
         products(tmem + kTXi, dBk, 32, kTileBytes, NB, dS, 2048, 8192, 3 * NB, kIdY, false);   // B dS^T, three parts
+        tc::commit(&tl.xi_full);
         products(tmem + kTdB, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, true);                // dB += (d out X) dS, two parts
         tc::commit(&tl.e_full);
       }
@@ -206,9 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
     bool ok = true;
     // the state (or its gradient) of this thread into three bf16 parts, the smallest first: the tensor core cuts its sums
     // off below their leading bits, which the large part then meets in its own steps only
-    auto parts = [&](const float* src, float (&v)[PP]) {
+    auto fetch = [&](const float* src, float (&v)[PP]) {
 #pragma unroll
       for (int q = 0; q < PP; ++q) v[q] = __ldg(src + (sp + q) * N + sn);
+    };
+    auto parts = [&](const float (&v)[PP]) {
 #pragma unroll
       for (int j = 0; j < PP / 8; ++j) {
         uint32_t o[3][4];
@@ -245,13 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       __syncwarp();
       if (lane == 0) arrive(bar);
     };
+    float S[PP];   // this thread's part of the state, fetched a phase ahead
+    if (n > 0) fetch(p.ckpt + ((b * p.H + h0) * (nc + 1) + c) * 64 * N, S);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int64_t unit = b * p.H + h0 + i;
       const Decays& dec = tl.dec[i % 3];
-      // ---- A: S, in dY (the last head's products with both buffers are done: this warp has seen e_full)
-      float S[PP];
-      parts(p.ckpt + (unit * (nc + 1) + c) * 64 * N, S);
+      // ---- A: S, in dY
+      if (i > 0 && !(ok = wait.warp(&tl.e_full, ph(i - 1)))) break;   // the last head's products with both buffers are done
+      parts(S);
       if (!(ok = wait.warp(&tl.dec_full[i % 3], unsigned(i / 3) & 1u) && wait.warp(&tl.xy_full, ph(i)))) break;
       const float in = dec.in[row], out = dec.out[row], d = dec.d[row], gam = dec.total;
       scaled(SM::kdY, in);
@@ -283,7 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
             }
           } else if (c0 < 32 * w + 32) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) L[e] = c0 + e >= row ? ex2((dec.hi[c0 + e] - hi) + (dec.lo[c0 + e] - lo)) : 0.f;
+            for (int e = 0; e < 16; ++e) {   // (the exponent is masked, not the result: no branch around the exponential)
+              const float x = (dec.hi[c0 + e] - hi) + (dec.lo[c0 + e] - lo);
+              L[e] = ex2(c0 + e >= row ? x : -1e30f);
+            }
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) L[e] = fs * far[c0 + e];
@@ -293,13 +301,18 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
             for (int e = 0; e < 16; ++e) L[e] = row >= dec.start[c0 + e] ? L[e] : 0.f;
           tc::wait_ld();
           if (c0 < 32 * w + 32) {   // the token itself: its part of (L o G) and of W is handled in fp32
+            float og = 0.f, ok_ = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c0 + e == row) {
-                tl.own_g[row] = gv[e];
-                tl.own_k[row] = kv[e];
-                gv[e] = 0.f;
-              }
+            for (int e = 0; e < 16; ++e) {
+              const bool me = c0 + e == row;
+              og = me ? gv[e] : og;
+              ok_ = me ? kv[e] : ok_;
+              gv[e] = me ? 0.f : gv[e];
+            }
+            if (row >> 4 == c0 >> 4) {
+              tl.own_g[row] = og;
+              tl.own_k[row] = ok_;
+            }
           }
           uint32_t m[8];
 #pragma unroll
@@ -345,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       double sds;
       {
         float dS[PP];
-        parts(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, dS);
+        fetch(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, dS);
+        parts(dS);
         float a = 0.f;
 #pragma unroll
         for (int q = 0; q < PP; ++q) a = fmaf(S[q], dS[q], a);
@@ -375,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       if (!(ok = wait.warp(&tl.m_done, ph(i)))) break;
       __syncwarp();
       if (lane == 0) arrive(&tl.xy_free);
-      if (!(ok = wait.warp(&tl.e_full, ph(i)))) break;
+      if (i + 1 < n) fetch(p.ckpt + (unit + 1) * (nc + 1) * 64 * N + c * 64 * N, S);   // the next head's state, under way
+      if (!(ok = wait.warp(&tl.xi_full, ph(i)))) break;
       tc::fence_after_sync();
       const int64_t t = t0 + row;
       {
@@ -430,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         if (lane == 0) reinterpret_cast<double*>(p.scratch + sc.anchor)[unit * nc + c] = double(gam) * s;
       }
     }
-    // ---- dB and dC: all products are done (every warp has seen the last e_full)
+    // ---- dB and dC
+    if (ok && n > 0) ok = wait.warp(&tl.e_full, ph(n - 1));
     if (ok) {
       tc::fence_after_sync();
       const int64_t t = t0 + row, at = ((b * p.T + t) * p.G + g) * N;
