@@ -7,6 +7,8 @@
 // channels and a run of tokens, so the window stays in registers and every input element is loaded once per run
 // plus W - 1 tokens of run-in (in L2: the neighbouring run has just read them).  The run length is chosen so
 // that the grid still fills the machine: long runs save run-in, short ones keep small calls parallel.
+#include <type_traits>
+
 #include "kernels.h"
 #include "layer_util.cuh"
 #include "state_space.h"
@@ -172,81 +174,121 @@ __global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p,
   float dw[W][V] = {}, dbias[V] = {};
   const T* x = static_cast<const T*>(p.x) + b * p.T * p.x_ld + d0;
   const T* dy = static_cast<const T*>(p.dy) + b * p.T * p.D + d0;
-  const int64_t tend = t1 + W - 1;
-  for (int64_t t = t0; t < tend; t += kBatch) {
-    typename VT::R rx[kBatch], rd[kBatch];
-    bool cut[kBatch];
+  const uint8_t* reset = p.reset ? p.reset + b * p.T : nullptr;
+  T* dx = static_cast<T*>(p.dx) + b * p.T * p.D + d0;
+  // One token: the gradient of u_t, which goes to the filter and to the inputs behind its taps; then the input that is
+  // W - 1 tokens back is complete.  PLAIN: a token of this run, all of whose taps count, and that input is of this run too.
+  auto token = [&](const typename VT::R& rx, const typename VT::R& rg, int64_t t, auto plain) {
+    constexpr bool PLAIN = decltype(plain)::value;
+    float v[V], g[V];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (t + i < tend && t + i < p.T) {
-        rx[i] = VT::load(x + (t + i) * p.x_ld);
-        rd[i] = VT::load(dy + (t + i) * p.D);
-        cut[i] = p.reset && p.reset[b * p.T + t + i];
-      }
+    for (int j = W - 1; j > 0; --j)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int64_t tt = t + i;
-      if (tt >= tend) break;
+      for (int e = 0; e < V; ++e) dxp[j][e] = dxp[j - 1][e];
 #pragma unroll
-      for (int j = W - 1; j > 0; --j)
+    for (int e = 0; e < V; ++e) dxp[0][e] = 0.f;
+    if (PLAIN || t < p.T) {
+      VT::get(rx, v);
+      VT::get(rg, g);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dxp[j][e] = dxp[j - 1][e];
+      for (int e = 0; e < V; e += 2) {
+        const float2 v2 = make_float2(v[e], v[e + 1]);
+        float2 g2 = make_float2(g[e], g[e + 1]);
+        auto at = [&](float (&a)[V]) -> float2& { return *reinterpret_cast<float2*>(&a[e]); };
+        if (SILU) {
+          float2 u = fma2(at(w[0]), v2, at(bias));
 #pragma unroll
-      for (int e = 0; e < V; ++e) dxp[0][e] = 0.f;
-      if (tt < p.T) {
-        float v[V], g[V];
-        VT::get(rx[i], v);
-        VT::get(rd[i], g);
-        if (cut[i]) {
-          age = 0;
+          for (int j = 1; j < W; ++j) u = fma2(at(w[j]), at(win[j - 1]), u);
+          const float sx = sigmoid_of<T>(u.x), sy = sigmoid_of<T>(u.y);
+          g2.x *= sx * fmaf(u.x, 1.f - sx, 1.f);
+          g2.y *= sy * fmaf(u.y, 1.f - sy, 1.f);
+        }
+        if (PLAIN || t < t1) {
+          at(dbias) = add2(at(dbias), g2);
+          at(dw[0]) = fma2(g2, v2, at(dw[0]));
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-            for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-        } else if (age < kNoReset) {
-          ++age;
+          for (int j = 1; j < W; ++j) at(dw[j]) = fma2(g2, at(win[j - 1]), at(dw[j]));
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (SILU) {
-            float u = fmaf(w[0][e], v[e], bias[e]);
+        for (int j = 0; j < W; ++j)
+          if (PLAIN || j <= age) at(dxp[j]) = fma2(at(w[j]), g2, at(dxp[j]));
 #pragma unroll
-            for (int j = 1; j < W; ++j) u = fmaf(w[j][e], win[j - 1][e], u);
-            const float s = sigmoid_of<T>(u);
-            g[e] *= s * fmaf(u, 1.f - s, 1.f);
-          }
-          if (tt < t1) {
-            dbias[e] += g[e];
-            dw[0][e] = fmaf(g[e], v[e], dw[0][e]);
-#pragma unroll
-            for (int j = 1; j < W; ++j) dw[j][e] = fmaf(g[e], win[j - 1][e], dw[j][e]);
-          }
-#pragma unroll
-          for (int j = 0; j < W; ++j)
-            if (j <= age) dxp[j][e] = fmaf(w[j][e], g[e], dxp[j][e]);
-#pragma unroll
-          for (int j = W - 2; j > 0; --j) win[j][e] = win[j - 1][e];
-          win[0][e] = v[e];
-        }
-      }
-      const int64_t td = tt - (W - 1);   // token whose gradient is now complete
-      if (td >= t0 || (t0 == 0 && td < 0)) {
-        if (td >= p.T) break;
-        if (p.dsT && td >= p.T - (W - 1) && p.T - 1 - td <= age) {   // it is in s_out, not cut off
-          float g[V];
-          VT::get(VT::load(static_cast<const T*>(p.dsT) + (b * (W - 1) + td - (p.T - (W - 1))) * p.D + d0), g);
-#pragma unroll
-          for (int e = 0; e < V; ++e) dxp[W - 1][e] += g[e];
-        }
-        if (td >= 0) {
-          if (range_ok((b * p.T + td) * p.D + d0, V, p.B * p.T * p.D, p.status))
-            VT::store(static_cast<T*>(p.dx) + (b * p.T + td) * p.D + d0, dxp[W - 1]);
-        } else if (p.ds0) {
-          VT::store(static_cast<T*>(p.ds0) + (b * (W - 1) + W - 1 + td) * p.D + d0, dxp[W - 1]);
-        }
+        for (int j = W - 2; j > 0; --j) at(win[j]) = at(win[j - 1]);
+        at(win[0]) = v2;
       }
     }
+    const int64_t td = t - (W - 1);
+    if (PLAIN) {
+      if (range_ok((b * p.T + td) * p.D + d0, V, p.B * p.T * p.D, p.status)) VT::store(dx + td * p.D, dxp[W - 1]);
+      return;
+    }
+    if (td < t0 && !(t0 == 0 && td < 0)) return;
+    if (p.dsT && td >= p.T - (W - 1) && p.T - 1 - td <= age) {   // it is in s_out, not cut off
+      float s[V];
+      VT::get(VT::load(static_cast<const T*>(p.dsT) + (b * (W - 1) + td - (p.T - (W - 1))) * p.D + d0), s);
+#pragma unroll
+      for (int e = 0; e < V; ++e) dxp[W - 1][e] += s[e];
+    }
+    if (td >= 0) {
+      if (range_ok((b * p.T + td) * p.D + d0, V, p.B * p.T * p.D, p.status)) VT::store(dx + td * p.D, dxp[W - 1]);
+    } else if (p.ds0) {
+      VT::store(static_cast<T*>(p.ds0) + (b * (W - 1) + W - 1 + td) * p.D + d0, dxp[W - 1]);
+    }
+  };
+  auto slow = [&](int64_t t) {   // any token, also behind the run or the row
+    typename VT::R rx{}, rg{};
+    if (t < p.T) {
+      rx = VT::load(x + t * p.x_ld);
+      rg = VT::load(dy + t * p.D);
+      if (reset && reset[t]) {
+        age = 0;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int e = 0; e < V; ++e) win[j][e] = 0.f;
+      } else if (age < kNoReset) {
+        ++age;
+      }
+    }
+    token(rx, rg, t, std::false_type{});
+  };
+  const int64_t tend = t1 + W - 1;
+  const int64_t plain_end = p.dsT ? min64(t1, p.T - (W - 1)) : t1;   // behind it an input may be part of s_out
+  int64_t t = t0;
+#pragma unroll 1
+  for (; t < min64(t0 + W - 1, tend); ++t) slow(t);
+  typename VT::R nx[kBatch], ng[kBatch];   // loads run one batch ahead
+  auto ahead = [&](int64_t t) {
+    if (t + kBatch <= plain_end)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        nx[i] = VT::load(x + (t + i) * p.x_ld);
+        ng[i] = VT::load(dy + (t + i) * p.D);
+      }
+  };
+  ahead(t);
+#pragma unroll 1
+  for (; t + kBatch <= plain_end; t += kBatch) {
+    typename VT::R rx[kBatch], rg[kBatch];
+    bool cut = false;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      rx[i] = nx[i];
+      rg[i] = ng[i];
+      cut |= reset && reset[t + i];
+    }
+    ahead(t + kBatch);
+    if (!cut && age >= W - 2) {   // (age counts the tokens since the last reset; the batch's first one adds one more)
+      age = min(age + kBatch, kNoReset);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) token(rx[i], rg[i], t + i, std::true_type{});
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kBatch; ++i) slow(t + i);
+    }
   }
+#pragma unroll 1
+  for (; t < tend; ++t) slow(t);
   if (p.scratch) {   // [run][W + 1][D]: dw of weight[.][0..W-1], then dbias
     float* o = p.scratch + br * (W + 1) * p.D + d0;
 #pragma unroll

@@ -6,9 +6,10 @@
 //   gate: dx = dh silu(z), dz = dh x silu'(z).
 //
 // HBM-bound: every input is read once and every output written once.  A slice is held in the registers of TPS
-// threads (a power of two; 1, 2 or 4 16-byte vectors each), so both reductions and the outputs come from one
+// threads (1, 2 or 4 16-byte vectors each), so both reductions and the outputs come from one
 // read.  Up to 32 threads reduce by shuffles alone; wider slices add one pass through shared memory.  Short
-// slices share a CTA of 256 threads.
+// slices share a CTA of 128 threads; CTAs are that small so that several independent ones per SM cover each other's
+// reductions.
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -19,7 +20,7 @@ namespace wkv7 {
 namespace {
 
 enum Mode { kPlain = 0, kResidual = 1, kGate = 2 };
-constexpr int kCta = 256;
+constexpr int kCta = 128;
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100: its reciprocal and the scaled values stay finite
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ Pair slice_reduce(Pair v, int tps, float (*sm)[2]) {
     if (COUNT == 2) v.b += __shfl_xor_sync(0xffffffffu, v.b, o);
   }
   if (tps <= 32) return v;
-  const int warp = threadIdx.x >> 5, nw = tps >> 5, first = warp & ~(nw - 1);
+  const int warp = threadIdx.x >> 5, nw = tps >> 5, first = blockDim.x == tps ? 0 : warp & ~(nw - 1);
   __syncthreads();   // the last use of `sm` is over
   if ((threadIdx.x & 31) == 0) *reinterpret_cast<float2*>(sm[warp]) = make_float2(v.a, v.b);
   __syncthreads();
@@ -57,9 +58,13 @@ __device__ __forceinline__ Pair slice_reduce(Pair v, int tps, float (*sm)[2]) {
   return Pair{r.x, r.y};
 }
 
+// Threads of a CTA at most: slices have up to 64, 1024 and (L <= 16384) 16384 / V vectors with 1, 2 and 4 per thread.
+template <typename T, int VPT>
+constexpr int kMaxThreads = VPT == 1 ? kCta : VPT == 2 ? 512 : 16384 / Vec16<T>::n / 4;
+
 struct Shape {
   int64_t L, slices;   // channels of a slice; rows * groups
-  int tps, spc;        // threads per slice (a power of two), slices per CTA
+  int tps, spc;        // threads per slice, slices per CTA: with several, a slice has a power of two
   int log_tps;
   float inv_l;         // 1 / L
 };
@@ -78,11 +83,11 @@ __device__ __forceinline__ void store_e4m3(uint8_t* o, const float (&q)[V]) {
 }
 
 template <typename T, int VPT, int MODE, int QUANT>   // QUANT: 0 none, 1 per 128 channels, 2 per slice
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const RmsArgs p, const Shape s) {
+__global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsArgs p, const Shape s) {
   constexpr int V = Vec16<T>::n;
   using VT = VecOf<T, V>;
   __shared__ __align__(8) float sm[32][2];
-  const int lane = threadIdx.x & (s.tps - 1), sub = threadIdx.x >> s.log_tps;
+  const int sub = s.spc == 1 ? 0 : threadIdx.x >> s.log_tps, lane = threadIdx.x - sub * s.tps;
   const int64_t nv = s.L / V, total = p.rows * p.D;
   for (int64_t s0 = int64_t(blockIdx.x) * s.spc; s0 < s.slices; s0 += int64_t(gridDim.x) * s.spc) {
     const int64_t slice = s0 + sub;
@@ -179,51 +184,76 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta) rms_fwd_kernel(const R
 // Backward.  A CTA stays on one group of channels (blockIdx.x % groups), so a thread keeps its channels' dweight
 // in registers over all its rows; the CTA's sum goes to its row of scratch, and column_sums adds those rows.
 template <typename T, int VPT, bool GATE>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta, VPT == 4 ? 1 : 3) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
+__global__ void __launch_bounds__(kMaxThreads<T, VPT>, kMaxThreads<T, VPT> < 512 ? 512 / kMaxThreads<T, VPT> : 1) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
   constexpr int V = Vec16<T>::n;
   using VT = VecOf<T, V>;
   __shared__ __align__(8) float sm[32][2];
   extern __shared__ float acc[];   // [spc][L] when a CTA holds several slices
-  const int lane = threadIdx.x & (s.tps - 1), sub = threadIdx.x >> s.log_tps;
+  const int sub = s.spc == 1 ? 0 : threadIdx.x >> s.log_tps, lane = threadIdx.x - sub * s.tps;
   const int64_t nv = s.L / V, total = p.rows * p.D;
   const int64_t g = blockIdx.x % p.groups, blk = blockIdx.x / p.groups;
   float dw[VPT][V] = {};
-  float wt[VPT][V];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
+  // The weight stays in registers too, except with four vectors: it is read again, from the L1, for each row.
+  constexpr bool HOLD = VPT < 4;
+  float held[HOLD ? VPT : 1][V];
+  auto weight_of = [&](int i, float (&w)[V]) {
     const int64_t v = i * s.tps + lane;
 #pragma unroll
-    for (int e = 0; e < V; ++e) wt[i][e] = v < nv ? __ldg(p.weight + g * s.L + v * V + e) : 0.f;
-  }
+    for (int u = 0; u < V / 4; ++u) {
+      const float4 w4 = v < nv ? __ldg(reinterpret_cast<const float4*>(p.weight + g * s.L + v * V) + u) : make_float4(0, 0, 0, 0);
+      w[4 * u] = w4.x; w[4 * u + 1] = w4.y; w[4 * u + 2] = w4.z; w[4 * u + 3] = w4.w;
+    }
+  };
+  if (HOLD)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) weight_of(i, held[HOLD ? i : 0]);
+  // The next row's loads are under way while this one is reduced, except with four vectors, which take too
+  // many registers.
+  constexpr bool AHEAD = VPT < 4;
+  typename VT::R nx[VPT], nz[VPT], ng[VPT];
+  auto fetch = [&](int64_t row) {
+    const int64_t base = row * p.D + g * s.L;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int64_t v = i * s.tps + lane, o = base + v * V;
+      if (row < p.rows && v < nv && range_ok(o, V, total, p.status)) {
+        nx[i] = VT::load(static_cast<const T*>(p.x) + o);
+        ng[i] = VT::load(static_cast<const T*>(p.dout) + o);
+        if (GATE) nz[i] = VT::load(static_cast<const T*>(p.other) + o);
+        else if (p.dh) nz[i] = VT::load(static_cast<const T*>(p.dh) + o);
+      }
+    }
+  };
+  if (AHEAD) fetch(blk * s.spc + sub);
   for (int64_t r0 = blk * s.spc; r0 < p.rows; r0 += nb * s.spc) {
     const int64_t row = r0 + sub;
     const int64_t base = row * p.D + g * s.L;
     typename VT::R rx[VPT], rz[VPT], rg[VPT];
     bool act[VPT];
+    if (!AHEAD) fetch(row);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int64_t v = i * s.tps + lane, o = base + v * V;
-      act[i] = row < p.rows && v < nv && range_ok(o, V, total, p.status);
-      if (act[i]) {
-        rx[i] = VT::load(static_cast<const T*>(p.x) + o);
-        rg[i] = VT::load(static_cast<const T*>(p.dout) + o);
-        if (GATE) rz[i] = VT::load(static_cast<const T*>(p.other) + o);
-        else if (p.dh) rz[i] = VT::load(static_cast<const T*>(p.dh) + o);
-      }
+      const int64_t v = i * s.tps + lane;
+      act[i] = row < p.rows && v < nv && range_ok(base + v * V, V, total, p.status);
+      rx[i] = nx[i];
+      rg[i] = ng[i];
+      rz[i] = nz[i];
     }
+    if (AHEAD) fetch(row + nb * s.spc);
     float ss = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (act[i]) {
-        float x[V], z[V], d[V];
+        float x[V], z[V], d[V], wt[V];
         VT::get(rx[i], x);
         VT::get(rg[i], d);
+        if (!HOLD) weight_of(i, wt);
         if (GATE) VT::get(rz[i], z);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float h = GATE ? x[e] * (z[e] * sigmoid_of<T>(z[e])) : x[e];
           ss = fmaf(h, h, ss);
-          gh = fmaf(d[e] * wt[i][e], h, gh);
+          gh = fmaf(d[e] * (HOLD ? held[HOLD ? i : 0][e] : wt[e]), h, gh);
         }
       }
     const Pair r = slice_reduce<false, 2>(Pair{ss, gh}, s.tps, sm);
@@ -233,8 +263,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta, VPT == 4 ? 1 : 3) rms_
     for (int i = 0; i < VPT; ++i)
       if (act[i]) {
         const int64_t o = base + (i * s.tps + lane) * V;
-        float x[V], z[V], d[V], dx[V], dz[V];
+        float x[V], z[V], d[V], dx[V], dz[V], wt[V];
         VT::get(rx[i], x);
+        if (!HOLD) weight_of(i, wt);
         VT::get(rg[i], d);
         if (GATE || p.dh) VT::get(rz[i], z);
 #pragma unroll
@@ -242,7 +273,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : kCta, VPT == 4 ? 1 : 3) rms_
           const float sg = GATE ? sigmoid_of<T>(z[e]) : 0.f;
           const float h = GATE ? x[e] * (z[e] * sg) : x[e];
           dw[i][e] = fmaf(d[e], h * rstd, dw[i][e]);
-          float dh = rstd * (d[e] * wt[i][e] - h * m);
+          float dh = rstd * (d[e] * (HOLD ? held[HOLD ? i : 0][e] : wt[e]) - h * m);
           if (GATE) {
             dx[e] = dh * (z[e] * sg);
             dz[e] = dh * x[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
@@ -287,8 +318,8 @@ __global__ void __launch_bounds__(1024) rms_dw_kernel(const float* scratch, int6
   column_sums(scratch, rows, D, D, [&](int64_t c, float v) { dweight[c] = v; });
 }
 
-// Threads of a slice of nv vectors: one vector each up to 64 vectors, two up to 512, four above.
-int vectors_per_thread(int64_t nv) { return nv <= 64 ? 1 : nv <= 512 ? 2 : 4; }
+// Threads of a slice of nv vectors: one vector each up to 64 vectors, two up to 1024, four above.
+int vectors_per_thread(int64_t nv) { return nv <= 64 ? 1 : nv <= 1024 ? 2 : 4; }
 Shape shape_of(const RmsArgs& p, int64_t nv, int vpt) {
   Shape s;
   s.L = p.D / p.groups;
@@ -301,15 +332,16 @@ Shape shape_of(const RmsArgs& p, int64_t nv, int vpt) {
   }
   s.inv_l = 1.f / float(s.L);
   s.spc = s.tps < kCta ? kCta / s.tps : 1;
+  if (s.spc == 1) s.tps = int((nv + vpt * 32 - 1) / (vpt * 32)) * 32;   // whole warps, not all that the power of two has
   return s;
 }
 constexpr int64_t kFwdCtas = 148 * 16;   // grid-stride over the rest
-constexpr int64_t kBwdThreads = 148 * 768;   // resident threads of the backward at its 80 registers: one wave
 
-// CTAs per group of the backward: its scratch rows.
-int64_t bwd_blocks(int64_t rows, int64_t groups, int tps, int spc) {
-  const int64_t threads = int64_t(tps) * spc;
-  const int64_t cap = kBwdThreads / threads / groups, need = (rows + spc - 1) / spc;
+// CTAs per group of the backward, its scratch rows: one wave.  An SM holds 512 threads of the backward's 128 registers, or,
+// of the 32-bit kernel with four vectors, the 1024 of its 64.
+int64_t bwd_blocks(int64_t rows, int64_t groups, const Shape& s, bool wide) {
+  const int64_t per_sm = (wide ? 1024 : 512) / (int64_t(s.tps) * s.spc);
+  const int64_t cap = 148 * per_sm / groups, need = (rows + s.spc - 1) / s.spc;
   const int64_t nb = need < cap ? need : cap;
   return nb < 1 ? 1 : nb;
 }
@@ -332,9 +364,9 @@ cudaError_t fwd_mode(const RmsArgs& p, const Shape& s, cudaStream_t st) {
 }
 template <typename T, int VPT>
 cudaError_t bwd(const RmsArgs& p, const Shape& s, cudaStream_t st) {
-  const int64_t nb = bwd_blocks(p.rows, p.groups, s.tps, s.spc);
+  const int64_t nb = bwd_blocks(p.rows, p.groups, s, kMaxThreads<T, VPT> > 512);
   if (nb * p.groups > 2147483647) return cudaErrorInvalidValue;
-  const size_t smem = s.spc > 1 ? size_t(s.spc) * s.L * 4 : 0;   // at most 256 threads * 16 floats = 16 KiB
+  const size_t smem = s.spc > 1 ? size_t(s.spc) * s.L * 4 : 0;   // at most 128 threads * 16 floats = 8 KiB
   const dim3 grid(unsigned(nb * p.groups)), block(unsigned(s.tps * s.spc));
   if (p.other) rms_bwd_kernel<T, VPT, true><<<grid, block, smem, st>>>(p, s, nb);
   else rms_bwd_kernel<T, VPT, false><<<grid, block, smem, st>>>(p, s, nb);
@@ -371,8 +403,8 @@ int64_t rms_scratch_floats(int64_t rows, int64_t D, int64_t groups) {
     const int64_t nv = D / groups / n;
     RmsArgs p{};
     p.rows = rows; p.D = D; p.groups = groups;
-    const Shape s = shape_of(p, nv, vectors_per_thread(nv));
-    const int64_t nb = bwd_blocks(rows, groups, s.tps, s.spc);
+    const int vpt = vectors_per_thread(nv);
+    const int64_t nb = bwd_blocks(rows, groups, shape_of(p, nv, vpt), vpt == 4 && n == 4);
     most = nb > most ? nb : most;
   }
   return most * D;

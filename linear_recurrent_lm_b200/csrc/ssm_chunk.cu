@@ -439,11 +439,11 @@ cudaError_t run_n(const SsmArgs& p, const TileMaps& tm, const ChunkOp& op, cudaS
 
 }  // namespace
 
-// Runs that a row's chunks are cut into: with fewer rows of heads than SMs, as many as fill them, of at least 4 chunks.  A
+// Runs that a row's chunks are cut into: with fewer rows of heads than SMs, as many as fill them, of at least 2 chunks.  A
 // cut row is walked twice, first for the state that each run leaves (without the outputs' work), then from it on, so it
 // takes three runs to gain.
 int64_t ssm_segments(int64_t units, int64_t nc) {
-  const int64_t fit = units > 0 ? 148 / units : 1, most = nc / 4, k = fit < most ? fit : most;
+  const int64_t fit = units > 0 ? 148 / units : 1, most = nc / 2, k = fit < most ? fit : most;
   return k >= 3 ? k : 1;
 }
 int64_t ssm_segment_floats(int64_t B, int64_t T, int64_t H, int N) {
