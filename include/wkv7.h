@@ -452,7 +452,8 @@ wkv7_status_t wkv7_state_compose(const wkv7_desc_t* desc, const float* S, const 
  * side).  `ld` is the distance between consecutive tokens in elements, 0
  * means dense; rows of the batch are T * ld apart.  ld must be at least the
  * row's size and ld * sizeof(element) a multiple of 16 (dt: any ld >= H),
- * else WKV7_ERR_SHAPE / WKV7_ERR_ALIGN.  Outputs and gradients are dense.
+ * else WKV7_ERR_SHAPE / WKV7_ERR_ALIGN.  Outputs and gradients are dense, and
+ * overlap neither an input nor one another unless stated.
  */
 
 /*
@@ -492,7 +493,8 @@ wkv7_status_t wkv7_conv_forward(const wkv7_desc_t* desc, const wkv7_conv_t* cv, 
  * give dx [B,T,D], ds0 [B,W-1,D] (or NULL), and dweight fp32 [D,W], dbias
  * fp32 [D] (each may be NULL), which are written, not added to.  `scratch`
  * holds wkv7_conv_scratch_bytes(desc, cv) bytes (required when dweight or
- * dbias is asked for and T > 0: WKV7_ERR_WORKSPACE).
+ * dbias is asked for and T > 0: WKV7_ERR_WORKSPACE).  ds0 must not be dsT
+ * (WKV7_ERR_UNSUPPORTED).
  */
 size_t wkv7_conv_scratch_bytes(const wkv7_desc_t* desc, const wkv7_conv_t* cv);
 wkv7_status_t wkv7_conv_backward(const wkv7_desc_t* desc, const wkv7_conv_t* cv, const void* x, const void* s0,
@@ -522,10 +524,19 @@ wkv7_status_t wkv7_conv_step(const wkv7_desc_t* desc, const wkv7_conv_t* cv, con
  *   x        in   [B,T,H,64] desc->dtype;  dt  in  [B,T,H];  b, c  in  [B,T,G,N]
  *   s0       in   [B,H,64,N] fp32 or NULL for zeros
  *   reset    in   [B,T] u8 or NULL
- *   y        out  [B,T,H,64];  s_out  out  [B,H,64,N] fp32 or NULL
+ *   y        out  [B,T,H,64];  s_out  out  [B,H,64,N] fp32 or NULL; must not
+ *                 be s0 (WKV7_ERR_UNSUPPORTED)
  *   workspace out wkv7_ssm_workspace_bytes(desc, sp) bytes: the state before
  *            every 128th token, for the backward, then scratch; or NULL
- *            (nothing is kept, and CHUNKED cannot split a long sequence of few heads).
+ *            (nothing is kept, and a long sequence of few heads is not split
+ *            over the GPU)
+ *
+ * dt = -infinity with softplus is a step of zero: the token leaves the state
+ * as it is.  A NaN or infinity in a token reaches what the formulas make of
+ * it under SCAN, and nothing across a reset.  CHUNKED multiplies whole chunks
+ * with masked weights of zero, so there it may reach every output of its
+ * 128-token chunk, earlier tokens included, and the states and chunks after
+ * it: fill padding with finite values.
  */
 typedef struct {
   int64_t G;            /* groups: heads that share b and c are consecutive; H % G == 0 */
@@ -543,13 +554,14 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, co
 
 /*
  * Reverse mode, from the workspace that the forward of the same arguments
- * wrote (the algo may differ): dy [B,T,H,64], dsT [B,H,64,N] fp32 (gradient of
+ * wrote (the algo may differ: only the states are read): dy [B,T,H,64], dsT [B,H,64,N] fp32 (gradient of
  * s_out, or NULL) give dx [B,T,H,64], ddt [B,T,H], db, dc [B,T,G,N] (desc->dtype; db and dc
  * are summed over the group's heads), dA [H], dD [H], ddt_bias [H] fp32 (each
  * may be NULL) and ds0 [B,H,64,N] fp32 (or NULL).  All are written, not added
  * to.  ddt is the gradient of the dt input (before the bias and softplus).
  * `scratch` holds wkv7_ssm_scratch_bytes(desc, sp) bytes
- * (WKV7_ERR_WORKSPACE if it or the workspace is NULL when T > 0).
+ * (WKV7_ERR_WORKSPACE if it or the workspace is NULL when T > 0).  ds0 must
+ * not be dsT (WKV7_ERR_UNSUPPORTED).
  */
 size_t wkv7_ssm_scratch_bytes(const wkv7_desc_t* desc, const wkv7_ssm_t* sp);
 wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const void* x, const void* dt,

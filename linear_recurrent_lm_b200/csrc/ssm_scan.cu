@@ -11,6 +11,9 @@
 // is kept apart from `past`: the gradient of the decays is made of the paths between different tokens alone, and
 // where little is remembered they are far smaller than the own term that would absorb them.
 //
+// A decay of zero (a reset) drops what it is applied to instead of scaling it, so that nothing of the tokens behind it
+// is left, not even a NaN.
+//
 // FP32-bound: 3 R K operations per token and head (decay, output, update) against about 260 bytes.  One CTA per (b, h);
 // a thread owns 2 rows and every eighth 16-byte vector of the columns, so a token's K-vectors are read from shared
 // memory as whole 128-byte lines and the output needs three shuffles.  Tokens move in tiles: the next tile's loads are
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
 #pragma unroll
         for (int u = 0; u < NI; ++u)
 #pragma unroll
-          for (int e = 0; e < EV; ++e) Z[i][EV * u + e] = f * Z[i][EV * u + e] + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
+          for (int e = 0; e < EV; ++e) Z[i][EV * u + e] = (f == F(0) ? F(0) : f * Z[i][EV * u + e]) + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
     }
   F total = 1;
   auto put_state = [&](auto* dst, F f) {
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
 #pragma unroll
         for (int e = 0; e < EV; e += 2)
           *reinterpret_cast<D2*>(dst + (r0 + i) * K + (8 * u + lane8) * EV + e) =
-              D2{D(f * Z[i][EV * u + e]), D(f * Z[i][EV * u + e + 1])};
+              f == F(0) ? D2{} : D2{D(f * Z[i][EV * u + e]), D(f * Z[i][EV * u + e + 1])};
   };
   auto decay = [&](float d) -> F { return TR ? F(exp(double(d) * double(A))) : F(expf(d * A)); };
 
@@ -199,6 +202,9 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
       const int64_t t = token(pos0 + i);
       if (!LOCAL && op.chunk_state && (REV ? (t % kSsmChunk == kSsmChunk - 1 || t == T_ - 1) : t % kSsmChunk == 0))
         put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + t / kSsmChunk) * (R * K), REV ? f : F(1));
+      if (f == F(0))
+#pragma unroll
+        for (int e = 0; e < NI * EV; ++e) Z[0][e] = Z[1][e] = F(0);
       const F in = s_i[buf][i];
       const F2 rv = *reinterpret_cast<const F2*>(&s_r[buf][i][r0]);
       const F u0 = in * rv.x, u1 = in * rv.y;

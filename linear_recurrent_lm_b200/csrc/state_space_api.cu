@@ -183,6 +183,7 @@ wkv7_status_t wkv7_conv_backward(const wkv7_desc_t* d, const wkv7_conv_t* cv, co
   TRY(check_ptrs(false, {s0, dsT, ds0, scratch, dweight, dbias}));
   const bool want = dweight || dbias;
   if (n > 0 && want && !scratch) return WKV7_ERR_WORKSPACE;
+  if (n > 0 && ds0 && ds0 == dsT) return WKV7_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) {
     const bool ok = zero(dweight, cv->D * cv->W * 4, s) && zero(dbias, cv->D * 4, s) && copy(ds0, dsT, st * elt(d), s);
@@ -210,12 +211,13 @@ wkv7_status_t wkv7_conv_step(const wkv7_desc_t* d, const wkv7_conv_t* cv, const 
   return finish(d, wkv7::launch_conv_step(a, d->dtype, s), {{y, n, d->dtype}, {state, n * (cv->W - 1), d->dtype}}, a.status, s);
 }
 
-// The workspace: nc + 1 states per (b, h), then the chunked forward's segments.
+// The workspace: nc + 1 states per (b, h), which are all that the backward reads, then the segments of the forward's form.
 size_t wkv7_ssm_workspace_bytes(const wkv7_desc_t* d, const wkv7_ssm_t* sp) {
   wkv7::SsmArgs a;
   if (check_ssm(d, sp, &a, true) != WKV7_OK || d->T == 0) return 0;
   const int64_t nc = (d->T + wkv7::kSsmChunk - 1) / wkv7::kSsmChunk;
-  return size_t(d->B * d->H * (nc + 1) * wkv7::kHeadP * d->N + (chunked(d) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : wkv7::ssm_run_floats(d->B, d->T, d->H, d->N))) * 4;
+  return size_t(d->B * d->H * (nc + 1) * wkv7::kHeadP * d->N +
+                (chunked(d) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : wkv7::ssm_run_floats(d->B, d->T, d->H, d->N))) * 4;
 }
 
 wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const void* x, const void* dt, const void* b,
@@ -227,6 +229,7 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const
   TRY(check_ptrs(n > 0, {x, b, c, y}));
   TRY(check_ptrs(n > 0, {dt}, elt(d)));
   TRY(check_ptrs(false, {s0, s_out, workspace}));
+  if (n > 0 && s_out && s_out == s0) return WKV7_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (units == 0) return WKV7_OK;
   if (d->T == 0) return copy(s_out, s0, st * 4, s) ? WKV7_OK : WKV7_ERR_CUDA;
@@ -262,6 +265,7 @@ wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, cons
   TRY(check_ptrs(n > 0, {dt}, elt(d)));
   TRY(check_ptrs(false, {s0, dsT, ds0, workspace, scratch, dA, dD, ddt_bias}));
   if (n > 0 && (!workspace || !scratch)) return WKV7_ERR_WORKSPACE;
+  if (n > 0 && ds0 && ds0 == dsT) return WKV7_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) {   // no tokens: the parameters have no gradient, the state's passes through
     const bool ok = zero(dA, d->H * 4, s) && zero(dD, d->H * 4, s) && zero(ddt_bias, d->H * 4, s) && copy(ds0, dsT, st * 4, s);

@@ -599,7 +599,9 @@ def ssm_forward(x, dt, A, b, c, D=None, dt_bias=None, s0=None, reset=None, *, so
     """Selective state space scan: d = softplus(dt + dt_bias), S_t = exp(d A) S_{t-1} + d x_t b_t^T, y_t = S_t c_t + D x_t.
 
     x [B,T,H,64], dt [B,T,H], b, c [B,T,G,N] (H / G consecutive heads share a group; N = 64 or 128; token rows may be
-    slices of wider ones), A, D, dt_bias fp32 [H], s0 fp32 [B,H,64,N], reset [B,T].  Returns (y, s_out, workspace)."""
+    slices of wider ones), A, D, dt_bias fp32 [H], s0 fp32 [B,H,64,N], reset [B,T].  algo "auto" is "chunked" (tensor
+    cores) for bf16 and "scan" (token order) else; under "chunked" a NaN or infinity in a token may reach every output of
+    its 128-token chunk, so fill padding with finite values.  Returns (y, s_out, workspace)."""
     d, sp, ptrs, (B, T, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 2, algo, flags)
     y = _out(y, "y", (B, T, H, N_HEAD), x.dtype, x)
     if s_out is not None or want_state:
@@ -633,9 +635,9 @@ def ssm_backward(x, dt, A, b, c, dy, workspace, D=None, dt_bias=None, s0=None, r
             g[n] = _out(g.get(n), n, (H,), torch.float32, x)
     if want_ds0:
         g["ds0"] = _out(g.get("ds0"), "ds0", (B, H, N_HEAD, N), torch.float32, x)
-    need = int(lib().wkv7_ssm_workspace_bytes(d, sp))
+    need = 4 * B * H * (-(-T // 128) + 1) * N_HEAD * N if T else 0   # the states alone, whichever form wrote them
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"the backward needs the forward's workspace of {need} bytes")
+        raise ValueError(f"the backward needs the forward's workspace of at least {need} bytes")
     tmp = _scratch(lib().wkv7_ssm_scratch_bytes(d, sp), x)
     st = lib().wkv7_ssm_backward(d, sp, *ptrs, _dense(s0, "s0", (B, H, N_HEAD, N), torch.float32, x),
                                  _mask(reset, "reset", (B, T), x), _dense(dy, "dy", (B, T, H, N_HEAD), x.dtype, x),

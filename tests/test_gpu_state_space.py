@@ -317,6 +317,100 @@ def test_ssm_steps_follow_the_forward(W, dtype, N, G):
     assert not torch.equal(state[active], keep[active])
 
 
+def test_ssm_backward_takes_either_workspace(W):
+    """The states that one form's forward leaves serve the other form's backward."""
+    import torch
+    rng = np.random.default_rng(252)
+    dev, _ = _ssm_case(rng, "bf16", 2, 300, 4, 1, 64)
+    dy = torch.randn(2, 300, 4, 64, device="cuda").bfloat16()
+    ws = {a: W.ssm_forward(**dev, algo=a)[2] for a in ("scan", "chunked")}
+    assert ws["scan"].numel() != ws["chunked"].numel()        # room for runs of tokens, or for none
+    want = W.ssm_backward(dy=dy, workspace=ws["scan"], algo="scan", **dev)
+    for back, forward in (("scan", "chunked"), ("chunked", "scan")):
+        g = W.ssm_backward(dy=dy, workspace=ws[forward], algo=back, **dev)
+        for n, t in g.items():
+            if t.dtype == torch.float32:
+                _close(t, _f64(want[n]), "f32", FP32, n)
+            else:
+                _near(t, want[n], n)
+    with pytest.raises(ValueError, match="workspace"):
+        W.ssm_backward(dy=dy, workspace=ws["scan"][:64], algo="scan", **dev)
+
+
+@pytest.mark.parametrize("dtype,algo", FORMS)
+def test_ssm_masked_steps(W, dtype, algo):
+    """dt = -inf, or the type's lowest value, is a step of zero: the token adds nothing, the state passes, ddt is zero."""
+    import torch
+    rng = np.random.default_rng(253)
+    dev, ref = _ssm_case(rng, dtype, 2, 150, 4, 2, 64)
+    dev["dt"][:, 100:] = -float("inf")
+    dev["dt"][1, 40:60] = torch.finfo(_t(dtype)).min
+    ref["dt"] = _f64(dev["dt"])
+    with np.errstate(over="ignore"):
+        _ssm_check(W, rng, dtype, algo, dev, ref)
+    dy = torch.ones(2, 150, 4, 64, device="cuda", dtype=_t(dtype))
+    _, _, ws = W.ssm_forward(**dev, algo=algo)
+    g = W.ssm_backward(dy=dy, workspace=ws, algo=algo, **dev)
+    for n in ("ddt", "db"):
+        assert not g[n][:, 100:].any() and not g[n][1, 40:60].any(), n
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T", (90, 700))
+def test_ssm_scan_keeps_what_is_not_finite_in_its_segment(W, dtype, T):
+    """In token order a NaN or infinity before a reset changes nothing after it, and no gradient crosses back."""
+    import torch
+    rng = np.random.default_rng(254)
+    dev, _ = _ssm_case(rng, dtype, 2, T, 4, 2, 64, reset=None, strided=False)
+    cut = T // 2 + 3
+    dev["reset"] = torch.zeros(2, T, dtype=torch.uint8, device="cuda")
+    dev["reset"][:, cut] = 1
+    dy = torch.randn(2, T, 4, 64, device="cuda").to(_t(dtype))
+    ds = torch.randn(2, 4, 64, 64, device="cuda")
+    y, s, ws = W.ssm_forward(**dev, algo="scan")
+    g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo="scan", **dev)
+    bad = {n: v.clone() if v is not None else None for n, v in dev.items()}
+    bad["x"][0, cut - 2, 1, 3] = float("nan")
+    bad["b"][0, 5, 0, 7] = float("inf")
+    bad["c"][1, 9, 1, 0] = float("nan")
+    bad["s0"][1, 2, 0, 0] = float("inf")
+    y2, s2, ws = W.ssm_forward(**bad, algo="scan")
+    g2 = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo="scan", **bad)
+    assert torch.equal(y2[:, cut:], y[:, cut:]) and torch.equal(s2, s) and not y2[:, :cut].isfinite().all()
+    for n in ("dx", "ddt", "db", "dc"):
+        assert torch.equal(g2[n][:, cut:], g[n][:, cut:]), n
+    late = dy.clone()
+    late[0, cut + 1] = float("nan")
+    _, _, ws = W.ssm_forward(**dev, algo="scan")
+    g2 = W.ssm_backward(dy=late, workspace=ws, dsT=ds, algo="scan", **dev)
+    for n in ("dx", "ddt", "db", "dc"):
+        assert torch.equal(g2[n][:, :cut], g[n][:, :cut]), n
+    assert torch.equal(g2["ds0"], g["ds0"])
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_conv_keeps_what_is_not_finite_in_its_window(W, dtype):
+    import torch
+    rng = np.random.default_rng(122)
+    x, _, k, _, _ = _conv_case(rng, dtype, 2, 40, 24, 4, None, True, False)
+    w, bias, s0 = (k[n][0] for n in ("weight", "bias", "s0"))
+    r = torch.zeros(2, 40, dtype=torch.uint8, device="cuda")
+    r[:, 21] = 1
+    dy = torch.randn(2, 40, 24, device="cuda").to(_t(dtype))
+    y, _ = W.conv_forward(x, w, bias, s0, r)
+    g = W.conv_backward(x, w, dy, bias, s0, r)
+    bad = x.clone()
+    bad[0, 20, 5], bad[1, 10, 7] = float("nan"), float("inf")
+    y2, _ = W.conv_forward(bad, w, bias, s0, r)
+    g2 = W.conv_backward(bad, w, dy, bias, s0, r)
+    touched = torch.zeros(2, 40, 24, dtype=torch.bool, device="cuda")      # outputs whose taps see the value
+    touched[0, 20, 5] = touched[1, 10:14, 7] = True
+    assert torch.equal(y2[~touched], y[~touched]) and not y2[0, 20, 5].isfinite()
+    back = torch.zeros_like(touched)                                        # inputs of those outputs
+    back[0, 17:21, 5] = back[1, 7:14, 7] = True
+    assert torch.equal(g2["dx"][~back], g["dx"][~back])
+
+
 @pytest.mark.parametrize("algo", ("scan", "chunked"))
 def test_ssm_repeats_bit_for_bit(W, algo):
     import torch

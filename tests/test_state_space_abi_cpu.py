@@ -53,6 +53,7 @@ def test_conv_refusals(L):
     assert lib.wkv7_conv_scratch_bytes(d, ok(weight=None)) > 0 and lib.wkv7_conv_scratch_bytes(d, ok(W=9)) == 0
     back = lambda desc, cv, dx=FAKE, dw=FAKE, sc=FAKE: lib.wkv7_conv_backward(desc, cv, FAKE, None, None, FAKE, None, dx, dw, None, None, sc, None)   # noqa: E731
     assert back(d, ok(), sc=None) == L.ERR_WORKSPACE and back(d, ok(), dx=None) == L.ERR_NULL and back(d, ok(), dw=FAKE + 4) == L.ERR_ALIGN
+    assert lib.wkv7_conv_backward(d, ok(), FAKE, None, None, FAKE, FAKE, FAKE, FAKE, None, FAKE, FAKE, None) == L.ERR_UNSUPPORTED   # ds0 is dsT
     step = lambda desc, cv, st=FAKE: lib.wkv7_conv_step(desc, cv, FAKE, st, None, FAKE, None)   # noqa: E731
     assert step(d, ok()) == L.ERR_UNSUPPORTED                      # T must be 1
     assert step(_desc(L, T=1), ok(), None) == L.ERR_NULL
@@ -98,6 +99,9 @@ def test_ssm_refusals(L):
         desc, sp(), FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, ws, dx, ddt, FAKE, FAKE, dA, None, None, None, sc, None)
     assert back(d, ws=None) == L.ERR_WORKSPACE and back(d, sc=None) == L.ERR_WORKSPACE and back(d, dx=None) == L.ERR_NULL
     assert back(d, ddt=FAKE + 2) == L.ERR_ALIGN and back(d, dA=FAKE + 4) == L.ERR_ALIGN
+    assert _ssm(L, d, sp(), s0=FAKE, s_out=FAKE) == L.ERR_UNSUPPORTED
+    assert lib.wkv7_ssm_backward(d, sp(), FAKE, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, FAKE,
+                                 FAKE, None) == L.ERR_UNSUPPORTED                     # ds0 is dsT
     step = lambda desc, st=FAKE: lib.wkv7_ssm_step(desc, sp(), FAKE, FAKE, FAKE, FAKE, st, None, FAKE, None)   # noqa: E731
     assert step(d) == L.ERR_UNSUPPORTED and step(_desc(L, T=1), None) == L.ERR_NULL
 
