@@ -17,10 +17,15 @@
 // and dB, dC accumulate in TMEM over them.  Sixteen warps work in the same phase (ssm_chunk.cu says why):
 //   A  S into bf16 parts, in_t dy_t          (while G and K are computed)
 //   W  G and K from TMEM: L o G back to TMEM, d L o K to shared memory, the sums
-//   B  dS into bf16 parts (once the products with S are done), d_s out_s x_s
-//   E  dX and the per-token scalars
+//   B  d_s out_s x_s, dS into bf16 parts (once the products with S are done)
+//   E  dX
+// while further warps issue MMAs (16), load tiles (17), prepare the decays (18) and, from the sums that the working warps
+// leave, write the per-token scalars of the head before (19).
 // TMEM: [0,128) G, then L o G as bf16 (64) and (L o G)^T dY (64); [128,256) K, then C S^T (64) and B dS^T (64); dB; dC.
-// MMA work per chunk and head at N = 128: 5600 cycles at the rates measured for these shapes.
+// What bounds it: phase W, by the instructions of one scheduler.  A warp reaches the TMEM lanes of its number modulo four,
+// which is its scheduler too, so the first quadrant's four warps share the eight 16-column units of the longest rows (550
+// instructions each, a third of them fp64): 5000 of about 19000 cycles per chunk and head; the others wait for them.
+// The MMA work is 5600 cycles at N = 128, at the rates measured for these shapes.  B=8 T=4096 H=32 N=128: 684 us.
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -29,7 +34,7 @@ namespace {
 
 using namespace stc;
 
-constexpr int kWorkers = 16, kDecayWarps = 2, kThreads = 32 * (kWorkers + 2 + kDecayWarps);
+constexpr int kWorkers = 16, kThreads = 32 * (kWorkers + 4);   // 20 warps of 96 registers; a 21st would leave 80
 constexpr uint32_t kTG = 0, kTM = 0, kTX1 = 64, kTK = 128, kTY2 = 128, kTXi = 192, kTdB = 256, kTdC = 384;
 
 template <int N>
@@ -45,12 +50,16 @@ struct Smem {
     float own_g[kQ], own_k[kQ];
     double sds[kWorkers];
     unsigned long long bc_full, xy_full, xy_free, gk_full, s_ready, w_ready, y2_full, m_done, ds_ready, xi_full, e_full, ab_free, quad[4],
-        dec_full[3], dec_free[3], drained;
+        dec_full[3], dec_free[3], sums_free, sc_free, drained;
     uint32_t tmem;
     int dead;
   };
   static constexpr int kBytes = kEnd + int(sizeof(Tail)) + 1024;
 };
+
+__device__ __forceinline__ void prefetch_l2(const float* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 // Sums of 16 values over the 32 lanes: lane l gets that of value l & 15.
 __device__ __forceinline__ double lane_sums(double (&v)[16]) {
@@ -88,14 +97,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
 
   if (threadIdx.x == 0) {
     tl.dead = 0;
-    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full, &tl.drained};
+    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full, &tl.sums_free, &tl.sc_free,
+                                 &tl.drained};
     for (auto* bar : one) mbar_init(bar, 1);
     unsigned long long* all[] = {&tl.xy_free, &tl.s_ready, &tl.w_ready, &tl.ds_ready, &tl.ab_free};
     for (auto* bar : all) mbar_init(bar, kWorkers);
     for (int i = 0; i < 4; ++i) mbar_init(&tl.quad[i], 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&tl.dec_full[i], 1);
-      mbar_init(&tl.dec_free[i], kWorkers);
+      mbar_init(&tl.dec_free[i], kWorkers + 1);
     }
   }
   // the half of (L o K)^T behind the diagonal blocks stays zero
@@ -121,7 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         tma_load_4d(sm + SM::kC + j * kTileBytes, &tm.c, 64 * j, int(g), t0, int(b), &tl.bc_full);
       }
       ++bc_loads;
+      auto ahead = [&](int i) {   // a head's state and its gradient into the L2
+        if (i >= n) return;
+        const int64_t unit = b * p.H + h0 + i;
+        prefetch_l2(p.ckpt + (unit * (nc + 1) + c) * 64 * N, 64 * N * 4);
+        prefetch_l2(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, 64 * N * 4);
+      };
+      ahead(0);
       for (int i = 0; i < n; ++i) {
+        ahead(i + 1);
         if (i >= 1 && !wait(&tl.xy_free, ph(i - 1))) break;
         mbar_arrive_expect_tx(&tl.xy_full, 2 * kTileBytes);
         tma_load_4d(sm + SM::kX, &tm.x, 0, int(h0 + i), t0, int(b), &tl.xy_full);
@@ -129,18 +147,58 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         ++xy_loads;
       }
     }
-  } else if (warp >= 18) {
+  } else if (warp == 19) {
+    // ------------------------------------------------------------ the per-token scalars, from the working warps' sums
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int64_t unit = b * p.H + h0 + i;
+      if (!(ok = wait.warp(&tl.dec_full[i % 3], unsigned(i / 3) & 1u) && wait.warp(&tl.ab_free, ph(i)))) break;
+      const Decays& dec = tl.dec[i % 3];
+      double row[4], col[4];   // all of it is read first: the working warps wait for that
+      float far[4], own[4], xdy[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int t = 32 * q + lane;
+        double rs = 0.0;
+#pragma unroll
+        for (int j = 0; j <= q; ++j) rs += tl.rowp[j][t];
+        row[q] = rs + double(dec.in[t] * ((tl.rp[0][t] + tl.rp[1][t]) + (tl.rp[2][t] + tl.rp[3][t])));
+        col[q] = (tl.colp[0][t] + tl.colp[1][t]) + (tl.colp[2][t] + tl.colp[3][t]);
+        far[q] = dec.out[t] * ((tl.fp[0][t] + tl.fp[1][t]) + (tl.fp[2][t] + tl.fp[3][t]));
+        xdy[q] = tl.own_k[t];
+        own[q] = tl.own_g[t] * xdy[q];
+      }
+      double s = lane < kWorkers ? tl.sds[lane] : 0.0;
+      const float gam = dec.total;
+      __syncwarp();
+      if (lane == 0) {
+        arrive(&tl.dec_free[i % 3]);
+        arrive(&tl.sums_free);
+      }
+      const int64_t o = unit * nc * kQ + t0 + lane;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        reinterpret_cast<double*>(p.scratch + sc.row)[o + 32 * q] = row[q];
+        reinterpret_cast<double*>(p.scratch + sc.col)[o + 32 * q] = col[q];
+        p.scratch[sc.far + o + 32 * q] = far[q];
+        p.scratch[sc.own + o + 32 * q] = own[q];
+        p.scratch[sc.xdy + o + 32 * q] = xdy[q];
+      }
+#pragma unroll
+      for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      if (lane == 0) reinterpret_cast<double*>(p.scratch + sc.anchor)[unit * nc + c] = double(gam) * s;
+    }
+  } else if (warp == 18) {
     // ------------------------------------------------------------ decays
     RawSteps raw;
-    const int first = warp - 18;
-    if (first < n) raw.load(p, b, h0 + first, c);
-    for (int i = first; i < n; i += kDecayWarps) {
+    if (n > 0) raw.load(p, b, h0, c);
+    for (int i = 0; i < n; ++i) {
       const float A = __ldg(p.A + h0 + i), bias = p.dt_bias ? __ldg(p.dt_bias + h0 + i) : 0.f;
       if (i >= 3 && !wait.warp(&tl.dec_free[i % 3], unsigned(i / 3 - 1) & 1u)) break;
       chunk_decays(p, A, bias, c, raw, true, tl.dec[i % 3]);
       __syncwarp();
       if (lane == 0) arrive(&tl.dec_full[i % 3]);
-      if (i + kDecayWarps < n) raw.load(p, b, h0 + i + kDecayWarps, c);
+      if (i + 1 < n) raw.load(p, b, h0 + i + 1, c);
     }
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue: one elected lane of a warp that stays together
@@ -172,8 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       __syncwarp();
       if (!(ok = wait.warp(&tl.s_ready, ph(i)))) break;
       tc::fence_after_sync();
-      if (elected())     // dC += (in dY) S, two parts
+      if (elected()) {   // dC += (in dY) S, two parts
         products(tmem + kTdC, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, i > 0);
+        tc::commit(&tl.sc_free);
+      }
       __syncwarp();
       if (!(ok = wait.warp(&tl.w_ready, ph(i)))) break;
       tc::fence_after_sync();
@@ -203,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
     const uint32_t lanes = tmem + (uint32_t(32 * w) << 16);
     const int sn = threadIdx.x % N, sp = threadIdx.x / N * PP;   // this thread's state column and first state row
     WarpBarrier quad{&tl.quad[w], 0};
-    const int64_t tp = nc * kQ;
     bool ok = true;
     // the state (or its gradient) of this thread into three bf16 parts, the smallest first: the tensor core cuts its sums
     // off below their leading bits, which the large part then meets in its own steps only
@@ -211,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
 #pragma unroll
       for (int q = 0; q < PP; ++q) v[q] = __ldg(src + (sp + q) * N + sn);
     };
-    auto parts = [&](const float (&v)[PP]) {
+    auto parts = [&](float (&v)[PP]) {
+#pragma unroll
+      for (int q = 0; q < PP; ++q) asm volatile("" : "+f"(v[q]));   // not before the wait in front: the loads run until here
 #pragma unroll
       for (int j = 0; j < PP / 8; ++j) {
         uint32_t o[3][4];
@@ -258,11 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       if (i > 0 && !(ok = wait.warp(&tl.e_full, ph(i - 1)))) break;   // the last head's products with both buffers are done
       parts(S);
       if (!(ok = wait.warp(&tl.dec_full[i % 3], unsigned(i / 3) & 1u) && wait.warp(&tl.xy_full, ph(i)))) break;
-      const float in = dec.in[row], out = dec.out[row], d = dec.d[row], gam = dec.total;
+      const float in = dec.in[row], out = dec.out[row], d = dec.d[row];
       scaled(SM::kdY, in);
       hand_over(&tl.s_ready);
       // ---- W: columns t of row s, 16 at a time from the diagonal block on
-      if (!(ok = wait.warp(&tl.gk_full, ph(i)))) break;
+      if (!(ok = wait.warp(&tl.gk_full, ph(i)) && (i == 0 || wait.warp(&tl.sums_free, ph(i - 1))))) break;
       tc::fence_after_sync();
       double col = 0.0;
       uint32_t ma[8], mb[8];
@@ -350,22 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       }
       tc::fence_before_sync();
       hand_over(&tl.w_ready);
-      // ---- B: dS, d out X (the products with S and the scaled dY are done)
+      // ---- B: d out X (the product with the scaled dY is done), dS (those with S are)
+      float S2[PP], dS[PP];   // S again, for <S, dS>: kept since phase A it would be 16 registers through W
+      fetch(p.ckpt + (unit * (nc + 1) + c) * 64 * N, S2);
+      fetch(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, dS);
+      if (!(ok = wait.warp(&tl.sc_free, ph(i)))) break;
+      scaled(SM::kX, d * out);
       if (!(ok = wait.warp(&tl.y2_full, ph(i)))) break;
       tc::fence_after_sync();
       float y2[16];
       ld16(lanes + kTY2 + 16 * r, y2);
       double sds;
       {
-        float dS[PP];
-        fetch(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, dS);
         parts(dS);
         float a = 0.f;
 #pragma unroll
-        for (int q = 0; q < PP; ++q) a = fmaf(S[q], dS[q], a);
+        for (int q = 0; q < PP; ++q) a = fmaf(S2[q], dS[q], a);
         sds = double(a);
       }
-      scaled(SM::kX, d * out);
       hand_over(&tl.ds_ready);
       // ---- E: this thread's 16 channels of x and dy, then the tiles may be loaded anew
       uint32_t xv[8], yv[8];
@@ -389,7 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       if (!(ok = wait.warp(&tl.m_done, ph(i)))) break;
       __syncwarp();
       if (lane == 0) arrive(&tl.xy_free);
-      if (i + 1 < n) fetch(p.ckpt + (unit + 1) * (nc + 1) * 64 * N + c * 64 * N, S);   // the next head's state, under way
       if (!(ok = wait.warp(&tl.xi_full, ph(i)))) break;
       tc::fence_after_sync();
       const int64_t t = t0 + row;
@@ -412,38 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
           o[k] = pack(q.x, q.y);
         }
         tl.fp[r][row] = a.x + a.y;
+        // (an arrival waits for the stores before it, so dX is stored behind these)
+        __syncwarp();
+        if (lane == 0) {
+          arrive(&tl.dec_free[i % 3]);
+          arrive(&tl.ab_free);
+        }
         if (t < p.T && range_ok(t, 1, p.T, p.status)) {
           uint4* dx = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx) + ((b * p.T + t) * p.H + h0 + i) * 64 + 16 * r);
           dx[0] = make_uint4(o[0], o[1], o[2], o[3]);
           dx[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
       }
-      if (!(ok = quad(wait))) break;
-      if (r == 0) {   // the per-token scalars
-        const int64_t o = unit * tp + t0 + row;
-        double rs = 0.0;
-        for (int j = 0; j <= w; ++j) rs += tl.rowp[j][row];
-        const float rr = (tl.rp[0][row] + tl.rp[1][row]) + (tl.rp[2][row] + tl.rp[3][row]);
-        const float ff = (tl.fp[0][row] + tl.fp[1][row]) + (tl.fp[2][row] + tl.fp[3][row]);
-        reinterpret_cast<double*>(p.scratch + sc.row)[o] = rs + double(in * rr);
-        reinterpret_cast<double*>(p.scratch + sc.col)[o] =
-            (tl.colp[0][row] + tl.colp[1][row]) + (tl.colp[2][row] + tl.colp[3][row]);
-        p.scratch[sc.far + o] = out * ff;
-        p.scratch[sc.own + o] = tl.own_g[row] * tl.own_k[row];
-        p.scratch[sc.xdy + o] = tl.own_k[row];
-      }
-      __syncwarp();
-      if (lane == 0) {
-        arrive(&tl.dec_free[i % 3]);
-        arrive(&tl.ab_free);
-      }
-      if (warp == 0) {
-        if (!(ok = wait.warp(&tl.ab_free, ph(i)))) break;   // every warp's share of <S, dS>
-        double s = lane < kWorkers ? tl.sds[lane] : 0.0;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) reinterpret_cast<double*>(p.scratch + sc.anchor)[unit * nc + c] = double(gam) * s;
-      }
+      if (i + 1 < n) fetch(p.ckpt + ((unit + 1) * (nc + 1) + c) * 64 * N, S);   // the next head's state, under way
     }
     // ---- dB and dC
     if (ok && n > 0) ok = wait.warp(&tl.e_full, ph(n - 1));
