@@ -519,7 +519,8 @@ wkv7_status_t wkv7_conv_step(const wkv7_desc_t* desc, const wkv7_conv_t* cv, con
  *   desc     B, T, H heads, N = 64 or 128 state channels, dtype, algo: SCAN
  *            (token order, any dtype), CHUNKED (128-token chunks on the tensor
  *            cores; bf16 only, else WKV7_ERR_UNSUPPORTED) or AUTO (CHUNKED
- *            for bf16, SCAN otherwise)
+ *            for bf16, but SCAN in the forward of at most 16 tokens; SCAN
+ *            otherwise)
  *   sp       below
  *   x        in   [B,T,H,64] desc->dtype;  dt  in  [B,T,H];  b, c  in  [B,T,G,N]
  *   s0       in   [B,H,64,N] fp32 or NULL for zeros
@@ -591,7 +592,7 @@ wkv7_status_t wkv7_ssm_step(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const
  *   desc     B, T, dtype (H and N ignored)
  *   rn       D channels; D % groups == 0, D / groups a multiple of 8 and at
  *            most 16384 (else WKV7_ERR_UNSUPPORTED); weight fp32 [D], 16-byte
- *            aligned; eps > 0
+ *            aligned; 0 < eps < 1e30
  *   x, other in   [B,T,D] desc->dtype (other may be NULL)
  *   h_out    out  [B,T,D]: required with gate == 0 and `other`, else NULL; may be x or other
  *   out      out  quant_block == 0: [B,T,D] desc->dtype.  Otherwise e4m3

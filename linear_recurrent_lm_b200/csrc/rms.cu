@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
 // Backward.  A CTA stays on one group of channels (blockIdx.x % groups), so a thread keeps its channels' dweight
 // in registers over all its rows; the CTA's sum goes to its row of scratch, and column_sums adds those rows.
 template <typename T, int VPT, bool GATE>
-__global__ void __launch_bounds__(kMaxThreads<T, VPT>, kMaxThreads<T, VPT> < 512 ? 512 / kMaxThreads<T, VPT> : 1) rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
+__global__ void __launch_bounds__(kMaxThreads<T, VPT>, kMaxThreads<T, VPT> < 512 ? 512 / kMaxThreads<T, VPT> : 1)
+rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
   constexpr int V = Vec16<T>::n;
   using VT = VecOf<T, V>;
   __shared__ __align__(8) float sm[32][2];

@@ -8,14 +8,14 @@
 // kernel serves both (REV), without the outputs (OUT = false).
 //
 // Precision: x, b, c enter the products as the bf16 they are; accumulators, decays and the carried state are fp32
-// (Lambda fp64).  What is rounded: M off its diagonal to bf16 (2^-9, like y itself); S as two bf16 parts in C S^T (2^-17); the weighted
-// x as three parts in the state's update (2^-25), so that states are fp32 results.
+// (Lambda fp64).  What is rounded: M off its diagonal to bf16 (2^-9, like y itself); S as two bf16 parts in C S^T
+// (2^-17); the weighted x as three parts in the state's update (2^-25), so that states are fp32 results.
 //
 // One CTA per (b, h) and segment of its chunks, one CTA per SM (its tiles fill the shared memory).  Sixteen warps work,
 // four per quadrant of TMEM lanes, all through the same phases of a chunk:
-//   M     thread = token row, 16 columns at a time, dealt to the quadrant's warps up to the diagonal.  G comes from TMEM, M goes back there as
-//         the A operand of M X; off the diagonal blocks the decay is a product of a row and a column factor, both relative
-//         to the row block's start (so at most one), which leaves 32 exponentials per row instead of 128
+//   M     thread = token row, 16 columns at a time, dealt to the quadrant's warps up to the diagonal.  G comes from TMEM, M
+//         goes back there as the A operand of M X; off the diagonal blocks the decay is a product of a row and a column
+//         factor, both relative to the row block's start (so at most one), which leaves 32 exponentials per row, not 128
 //   S     thread = state column, 16 fp32 rows of it in registers: add U, and write the bf16 parts for C S^T
 //   XS    thread = token row, a quarter of it: the weighted x in three bf16 parts
 //   Y     thread = token row, a quarter of it: Y1 + in Y2 + (D + M_tt) x, stored as whole 32-byte sectors
@@ -25,8 +25,9 @@
 // What bounds it: instruction fetch.  Code beyond the few KB of a scheduler's own cache arrives at 5.5 cycles per
 // instruction (measured on straight-line FMAs), once for all warps of the scheduler that run it together.  Roles on
 // separate warps (M, state, XS) therefore ran at 7300 to 11600 cycles per chunk; all warps in the same phase, loops rolled,
-// share the fetches.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes (an SS product of 64 columns is
-// bound by reading its A from shared memory): G 512, C S^T 784, M X 260, state 1176.
+// share the fetches: about 7000.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes
+// (a product of 64 columns with A in shared memory is bound by reading it): G 512, C S^T 784, M X 260, state 1176.
+// B=8 T=4096 H=32 N=128: 290 us (256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed state pass 194 us.
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -152,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
     const uint64_t dBk = desc(base + SM::kB, 16), dBm = desc(base + SM::kB, kTileBytes), dX = desc(base + SM::kX, 16);
     constexpr uint32_t kIdG = tc::idesc_bf16(128, 128, 0, 0), kIdY = tc::idesc_bf16(128, 64, 0, 1), kIdU = tc::idesc_bf16(N, 64, 1, 1);
     // q groups of four K steps: A `ka` bytes apart in the step and `ga` in the group (mod `wrap` groups), B likewise
-    auto products = [&](uint32_t d, uint64_t a, uint32_t ka, uint32_t ga, int wrap, uint64_t b, uint32_t kb, uint32_t gb, int q, uint32_t id,
-                        unsigned long long* done) {
+    auto products = [&](uint32_t d, uint64_t a, uint32_t ka, uint32_t ga, int wrap, uint64_t b, uint32_t kb, uint32_t gb, int q,
+                        uint32_t id, unsigned long long* done) {
       tc::fence_after_sync();
       if (elected()) {
 #pragma unroll 1

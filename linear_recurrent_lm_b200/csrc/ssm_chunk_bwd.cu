@@ -77,7 +77,8 @@ __device__ __forceinline__ double lane_sums(double (&v)[16]) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArgs p, const SsmScratch sc, const __grid_constant__ TileMaps tm) {
+__global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArgs p, const SsmScratch sc,
+                                                                      const __grid_constant__ TileMaps tm) {
   using SM = Smem<N>;
   constexpr int NB = SM::kNB, PP = 64 * N / (32 * kWorkers);   // state elements of a thread: PP rows of one column
   extern __shared__ uint8_t raw_smem[];
@@ -97,8 +98,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
 
   if (threadIdx.x == 0) {
     tl.dead = 0;
-    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full, &tl.sums_free, &tl.sc_free,
-                                 &tl.drained};
+    unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full,
+                                 &tl.sums_free, &tl.sc_free, &tl.drained};
     for (auto* bar : one) mbar_init(bar, 1);
     unsigned long long* all[] = {&tl.xy_free, &tl.s_ready, &tl.w_ready, &tl.ds_ready, &tl.ab_free};
     for (auto* bar : all) mbar_init(bar, kWorkers);
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       if (elected()) {
         products(tmem + kTXi, dBk, 32, kTileBytes, NB, dS, 2048, 8192, 3 * NB, kIdY, false);   // B dS^T, three parts
         tc::commit(&tl.xi_full);
-        products(tmem + kTdB, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, true);                // dB += (d out X) dS, two parts
+        products(tmem + kTdB, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, true);   // dB += (d out X) dS, two
         tc::commit(&tl.e_full);
       }
       __syncwarp();
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q)
-          *reinterpret_cast<uint4*>(sm + SM::kS + (2 - q) * SM::kPart + swz(sn, sp / 8 + j)) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+          *reinterpret_cast<uint4*>(sm + SM::kS + (2 - q) * SM::kPart + swz(sn, sp / 8 + j)) =
+              make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
       }
     };
     // this thread's 16 channels of its token row of `tile`, scaled, into the scaled tile

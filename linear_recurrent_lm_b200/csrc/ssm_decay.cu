@@ -49,7 +49,8 @@ __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmSc
       cs[i] = CHUNKED ? cols[i] + double(fr[i]) : cols[i];
       v[i] = rows[i] - double(d[i]) * cs[i];
       if (CHUNKED) leave += double(d[i]) * double(fr[i]);
-      if (p.reset && p.reset[b * p.T + t0 + i]) rst |= 1u << i;
+      // a decay that is zero cuts like a reset: what is left of its sums is rounding, which a large A would blow up
+      if ((p.reset && p.reset[b * p.T + t0 + i]) || expf(d[i] * A) == 0.f) rst |= 1u << i;
     }
   }
   cut = rst >> 1;   // token i ends its segment where token i + 1 is a reset
@@ -154,7 +155,7 @@ SsmScratch ssm_scratch(int64_t B, int64_t T, int64_t H, int64_t G, int N, bool c
     }
   } else {
     s.dstate = take(2 * B * H * nc * state);
-    s.seg = take(2 * ssm_run_floats(B, T, H, N));
+    s.seg = take(5 * ssm_run_floats(B, T, H, N));   // of three scans, two of them in fp64
     s.state_t = take(2 * B * H * (nc + 1) * state);
     s.dcp = take(2 * B * T * H * N);
     s.dbp = take(2 * B * T * H * N);

@@ -7,16 +7,18 @@
 //   dc:  forward, Z = S^T    (N x 64):  rin = b, kin = x, con = dy, i = d   -> past, per head
 //   dx:  reverse, Z = dS     (64 x N):  rin = dy, kin = c, con = b          -> d (past + (b.c) dy) + D dy
 //   db:  reverse, Z = dS^T   (N x 64):  rin = c, kin = dy, con = x          -> past, per head
-// In reverse f is the decay of the token after (the gradient passes through it on its way back).  A token's own term
-// is kept apart from `past`: the gradient of the decays is made of the paths between different tokens alone, and
+// In reverse f is the decay of the token after (the gradient passes through it on its way back).  The transposed scans
+// leave a token's own term out of `past`: the gradient of the decays is made of the paths between different tokens alone, and
 // where little is remembered they are far smaller than the own term that would absorb them.
 //
 // A decay of zero (a reset) drops what it is applied to instead of scaling it, so that nothing of the tokens behind it
 // is left, not even a NaN.
 //
-// FP32-bound: 3 R K operations per token and head (decay, output, update) against about 260 bytes.  One CTA per (b, h);
-// a thread owns 2 rows and every eighth 16-byte vector of the columns, so a token's K-vectors are read from shared
-// memory as whole 128-byte lines and the output needs three shuffles.  Tokens move in tiles: the next tile's loads are
+// Bound by shared memory and shuffles rather than by its 3 R K operations per token and head (decay, output, update).  One
+// CTA per (b, h); a thread owns 4 rows and every eighth 16-byte vector of the columns, so a token's K-vectors are read from
+// shared memory as whole 128-byte lines, each serves 16 rows of the warp, and the outputs of 4 rows need four shuffles
+// (two rows per thread: 61 us instead of 38 for bf16 B=64 T=16 H=32 N=64).  B=8 T=1024 H=32 fp32 forward: N=64 325 us, N=128
+// 486 us; backward, three scans, 1.41 ms and 2.76 ms.  Tokens move in tiles: the next tile's loads are
 // in flight while this one is computed.
 //
 // The two scans behind the decay's gradient (dc and db) run in fp64, at half the rate: that gradient is a sum of
@@ -41,10 +43,9 @@ struct ScanOp {
                                          // scans: fp64): [B,H,stride], or null
   int64_t chunk_stride;
   float* last;                           // [B,H,R,K]: Z after the walk (reverse: carried through token 0's decay), or null
-  // The walk may be cut into `segments` runs of `per` tokens: a first pass (`local`) leaves each run's end state from
+  // The walk may be cut into `segments` runs of `per` tokens: a first pass (LOCAL) leaves each run's end state from
   // zero and its total decay, and the second starts every run from what those before it left.
   int64_t segments, per;
-  bool local;
   void *seg_state, *seg_decay;           // [B,H,segments] states [R][K] and decays, fp32 (transposed scans: fp64)
 };
 
@@ -58,52 +59,46 @@ __device__ __forceinline__ void load_pair(const double* p, double (&v)[2]) {
   v[0] = f.x; v[1] = f.y;
 }
 
-// One 16-byte vector of columns of both rows: decay, output, update, own term.
-__device__ __forceinline__ void advance(float* z0, float* z1, const float (&k)[4], const float (&c)[4], float f, float u0,
-                                        float u1, float2& a0, float2& a1, float2& own) {
-  const float2 ff = make_float2(f, f), v0 = make_float2(u0, u0), v1 = make_float2(u1, u1);
+// One 16-byte vector of columns of one row: decay, update, output; the transposed scans' output is taken before the update.
+__device__ __forceinline__ void advance(float* z, const float (&k)[4], const float (&c)[4], float f, float u, float2& a) {
 #pragma unroll
   for (int e = 0; e < 4; e += 2) {
-    const float2 k2 = make_float2(k[e], k[e + 1]), c2 = make_float2(c[e], c[e + 1]);
-    float2 &s0 = *reinterpret_cast<float2*>(z0 + e), &s1 = *reinterpret_cast<float2*>(z1 + e);
-    s0 = mul2(s0, ff);
-    s1 = mul2(s1, ff);
-    a0 = fma2(s0, c2, a0);
-    a1 = fma2(s1, c2, a1);
-    s0 = fma2(v0, k2, s0);
-    s1 = fma2(v1, k2, s1);
-    own = fma2(k2, c2, own);
+    float2& v = *reinterpret_cast<float2*>(z + e);
+    v = fma2(make_float2(u, u), make_float2(k[e], k[e + 1]), mul2(v, make_float2(f, f)));
+    a = fma2(v, make_float2(c[e], c[e + 1]), a);
   }
 }
-__device__ __forceinline__ void advance(double* z0, double* z1, const double (&k)[2], const double (&c)[2], double f, double u0,
-                                        double u1, double2& a0, double2& a1, double2&) {
-  z0[0] *= f; z0[1] *= f; z1[0] *= f; z1[1] *= f;
-  a0.x = fma(z0[0], c[0], a0.x); a0.y = fma(z0[1], c[1], a0.y);
-  a1.x = fma(z1[0], c[0], a1.x); a1.y = fma(z1[1], c[1], a1.y);
-  z0[0] = fma(u0, k[0], z0[0]); z0[1] = fma(u0, k[1], z0[1]);
-  z1[0] = fma(u1, k[0], z1[0]); z1[1] = fma(u1, k[1], z1[1]);
+__device__ __forceinline__ void advance(double* z, const double (&k)[2], const double (&c)[2], double f, double u, double2& a) {
+  z[0] *= f; z[1] *= f;
+  a.x = fma(z[0], c[0], a.x); a.y = fma(z[1], c[1], a.y);
+  z[0] = fma(u, k[0], z[0]); z[1] = fma(u, k[1], z[1]);
 }
+
+constexpr int kRows = 4;   // state rows of a thread
 
 // TR: the transposed scans (R = N, K = 64), in double.
 template <typename T, int R, int K, bool REV, bool TR, bool LOCAL>
-__global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const ScanOp op) {
+__global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, const ScanOp op) {
   using F = typename std::conditional<TR, double, float>::type;
   using F2 = typename std::conditional<TR, double2, float2>::type;
   constexpr int kTile = TR ? 8 : 16, EV = 16 / int(sizeof(F)), NI = K / (8 * EV);
-  constexpr int V = Vec16<T>::n, NT = 4 * R;
+  constexpr int V = Vec16<T>::n, NT = 8 * R / kRows;
   constexpr int VR = R / V, VK = K / V, kVecs = kTile * (VR + 2 * VK), kPer = (kVecs + NT - 1) / NT;
   __shared__ __align__(16) F s_r[2][kTile][R], s_k[2][kTile][K], s_c[2][kTile][K];
-  __shared__ F s_f[2][kTile], s_i[2][kTile], s_o[2][kTile];
+  __shared__ __align__(16) F s_fio[2][kTile][4];   // decay, factor of the input, factor of the output
+  __shared__ unsigned s_special[2];                // tokens of the tile with a decay of zero or a state to store
   __shared__ __align__(16) F s_out[kTile][R];
-  const int tid = threadIdx.x, lane8 = tid & 7, r0 = (tid >> 3) * 2;
-  const int64_t unit = blockIdx.x / op.segments, seg = blockIdx.x - unit * op.segments, b = unit / p.H, h = unit - b * p.H, g = h / (p.H / p.G);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // see `launch`
+  const int tid = threadIdx.x, lane8 = tid & 7, r0 = (tid >> 3) * kRows;
+  const int64_t unit = blockIdx.x / op.segments, seg = blockIdx.x - unit * op.segments;
+  const int64_t b = unit / p.H, h = unit - b * p.H, g = h / (p.H / p.G);
   const int64_t T_ = p.T, first = seg * op.per, end = min64(first + op.per, T_);   // positions of the walk
   const float A = __ldg(p.A + h);
   const float skip = op.skip ? __ldg(op.skip + h) : 0.f;
 
-  F Z[2][NI * EV];
+  F Z[kRows][NI * EV];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < kRows; ++i)
 #pragma unroll
     for (int u = 0; u < NI; ++u)
 #pragma unroll
@@ -116,18 +111,21 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
       const F f = static_cast<const F*>(op.seg_decay)[j];
       const F* z = static_cast<const F*>(op.seg_state) + j * (R * K);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < kRows; ++i)
 #pragma unroll
         for (int u = 0; u < NI; ++u)
 #pragma unroll
-          for (int e = 0; e < EV; ++e) Z[i][EV * u + e] = (f == F(0) ? F(0) : f * Z[i][EV * u + e]) + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
+          for (int e = 0; e < EV; ++e) {
+            F& v = Z[i][EV * u + e];
+            v = (f == F(0) ? F(0) : f * v) + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
+          }
     }
   F total = 1;
   auto put_state = [&](auto* dst, F f) {
     using D = std::remove_pointer_t<decltype(dst)>;
     using D2 = typename std::conditional<sizeof(D) == 8, double2, float2>::type;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int u = 0; u < NI; ++u)
 #pragma unroll
@@ -139,7 +137,9 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
 
   uint4 raw[kPer];
   F tf = 0, ti = 0, to = 0;
+  bool special = false;
   auto token = [&](int64_t pos) { return REV ? T_ - 1 - pos : pos; };
+  auto stores = [&](int64_t t) { return REV ? t % kSsmChunk == kSsmChunk - 1 || t == T_ - 1 : t % kSsmChunk == 0; };
   auto fetch = [&](int64_t pos0) {
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
         }
       }
     }
+    special = false;
     if (tid < kTile && pos0 + tid < end) {
       const int64_t t = token(pos0 + tid), bt = b * T_ + t;
       const float d = step_of<T>(p, bt, h);
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
       else tf = decay(REV ? step_of<T>(p, bt + 1, h) : d);
       ti = op.scale_in ? d : 1.f;
       to = op.scale_out ? d : 1.f;
+      special = tf == F(0) || (!LOCAL && op.chunk_state && stores(t));
     }
   };
   auto stage = [&](int buf) {
@@ -182,10 +184,14 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
         for (int e = 0; e < V; e += 2) *reinterpret_cast<F2*>(dst + e) = F2{F(f[e]), F(f[e + 1])};
       }
     }
+    if (tid < 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, special);
+      if (tid == 0) s_special[buf] = m;
+    }
     if (tid < kTile) {
-      s_f[buf][tid] = tf;
-      s_i[buf][tid] = ti;
-      s_o[buf][tid] = to;
+      s_fio[buf][tid][0] = tf;
+      s_fio[buf][tid][1] = ti;
+      s_fio[buf][tid][2] = to;
     }
   };
 
@@ -196,43 +202,60 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
   for (int64_t pos0 = first; pos0 < end; pos0 += kTile, buf ^= 1) {
     const int n = int(min64(kTile, end - pos0));
     if (pos0 + kTile < end) fetch(pos0 + kTile);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const F f = s_f[buf][i];
-      const int64_t t = token(pos0 + i);
-      if (!LOCAL && op.chunk_state && (REV ? (t % kSsmChunk == kSsmChunk - 1 || t == T_ - 1) : t % kSsmChunk == 0))
-        put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + t / kSsmChunk) * (R * K), REV ? f : F(1));
-      if (f == F(0))
+    auto one = [&](int i, unsigned mark) {
+      const F f = s_fio[buf][i][0], in = s_fio[buf][i][1];
+      if (mark >> i & 1u) {
+        const int64_t t = token(pos0 + i);
+        if (!LOCAL && op.chunk_state && stores(t))
+          put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + t / kSsmChunk) * (R * K), REV ? f : F(1));
+        if (f == F(0))
 #pragma unroll
-        for (int e = 0; e < NI * EV; ++e) Z[0][e] = Z[1][e] = F(0);
-      const F in = s_i[buf][i];
-      const F2 rv = *reinterpret_cast<const F2*>(&s_r[buf][i][r0]);
-      const F u0 = in * rv.x, u1 = in * rv.y;
+          for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < NI * EV; ++e) Z[r][e] = F(0);
+      }
+      F u[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; r += 2) {
+        const F2 v = *reinterpret_cast<const F2*>(&s_r[buf][i][r0 + r]);
+        u[r] = in * v.x;
+        u[r + 1] = in * v.y;
+      }
       if (LOCAL) total *= f;
-      F2 a0{}, a1{}, own{};
+      F2 a[kRows] = {};
 #pragma unroll
-      for (int u = 0; u < NI; ++u) {
+      for (int q = 0; q < NI; ++q) {
         F k[EV], c[EV];
-        load_pair(&s_k[buf][i][(8 * u + lane8) * EV], k);
-        load_pair(&s_c[buf][i][(8 * u + lane8) * EV], c);
-        advance(&Z[0][EV * u], &Z[1][EV * u], k, c, f, u0, u1, a0, a1, own);   // (LOCAL: the outputs fall away)
-      }
-      if (LOCAL) continue;
-      F o0 = a0.x + a0.y, o1 = a1.x + a1.y, kc = own.x + own.y;
+        load_pair(&s_k[buf][i][(8 * q + lane8) * EV], k);
+        load_pair(&s_c[buf][i][(8 * q + lane8) * EV], c);
 #pragma unroll
-      for (int o = 1; o < 8; o *= 2) {
-        o0 += __shfl_xor_sync(0xffffffffu, o0, o);
-        o1 += __shfl_xor_sync(0xffffffffu, o1, o);
-        if (!TR) kc += __shfl_xor_sync(0xffffffffu, kc, o);
+        for (int r = 0; r < kRows; ++r) advance(&Z[r][EV * q], k, c, f, u[r], a[r]);   // (LOCAL: the outputs fall away)
       }
-      if (lane8 == 0) {
-        if (!TR) {
-          const F os = s_o[buf][i];
-          o0 = os * (kc * u0 + o0) + F(skip) * rv.x;
-          o1 = os * (kc * u1 + o1) + F(skip) * rv.y;
-        }
-        *reinterpret_cast<F2*>(&s_out[i][r0]) = F2{o0, o1};
+      if (LOCAL) return;
+      // sums over the 8 threads of the rows: each exchange halves the rows that a thread holds
+      const bool hi4 = lane8 & 4, hi2 = lane8 & 2;
+      F o[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) o[r] = a[r].x + a[r].y;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const F give = hi4 ? o[r] : o[r + 2];
+        o[r] = (hi4 ? o[r + 2] : o[r]) + __shfl_xor_sync(0xffffffffu, give, 4);
       }
+      const F give = hi2 ? o[0] : o[1];
+      F sum = (hi2 ? o[1] : o[0]) + __shfl_xor_sync(0xffffffffu, give, 2);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      if (!(lane8 & 1)) {
+        const int row = r0 + (lane8 >> 1);   // (bit 2 of the lane chose the pair of rows, bit 1 the row)
+        s_out[i][row] = TR ? sum : s_fio[buf][i][2] * sum + F(skip) * s_r[buf][i][row];
+      }
+    };
+    if (n == kTile && s_special[buf] == 0) {   // no branches between the tokens, so that they overlap
+#pragma unroll 4
+      for (int i = 0; i < kTile; ++i) one(i, 0);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) one(i, s_special[buf]);
     }
     if (pos0 + kTile < end) stage(buf ^ 1);
     __syncthreads();
@@ -259,39 +282,49 @@ __global__ void __launch_bounds__(4 * R) scan_kernel(const SsmArgs p, const Scan
   if (LOCAL) {
     put_state(static_cast<F*>(op.seg_state) + blockIdx.x * int64_t(R * K), F(1));
     if (tid == 0) static_cast<F*>(op.seg_decay)[blockIdx.x] = total;
-    return;
+  } else if (seg == op.segments - 1) {
+    if (op.last) {
+      F f = 1;
+      if (REV && T_ > 0) f = (p.reset && p.reset[b * T_]) ? F(0) : decay(step_of<T>(p, b * T_, h));
+      put_state(op.last + unit * (R * K), f);
+    }
+    if (!REV && op.chunk_state) put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + chunks_of(T_)) * (R * K), F(1));
   }
-  if (seg != op.segments - 1) return;
-  if (op.last) {
-    F f = 1;
-    if (REV && T_ > 0) f = (p.reset && p.reset[b * T_]) ? F(0) : decay(step_of<T>(p, b * T_, h));
-    put_state(op.last + unit * (R * K), f);
-  }
-  if (!REV && op.chunk_state) put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + chunks_of(T_)) * (R * K), F(1));
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // see `launch`
 }
 
 // Runs of a row's tokens: with fewer rows of heads than two per SM, as many as fill those slots, of at least 32 tokens.  A
-// cut row is walked twice, so it takes three runs to gain (B=2 T=512 H=12 N=64 fp32, forward: 140 us whole).
+// cut row is walked twice, so it takes three runs to gain (forward, N=64: B=2 T=512 H=12 fp32 34 us, 130 whole; B=1 T=96 H=32, three
+// runs, 19 us, 28 whole).
 int64_t scan_segments(int64_t units, int64_t T) {
   const int64_t fit = units > 0 ? 296 / units : 1, most = T / 32, k = fit < most ? fit : most;
   return k >= 3 ? k : 1;
 }
 
-template <typename T, int R, int K, bool REV, bool TR>
-cudaError_t scan(const SsmArgs& p, ScanOp op, float* seg, cudaStream_t s) {
+// One pass of a scan.  `beside`: it needs nothing of the launch before it, so it may start once that one's CTAs have all
+// started (programmatic dependent launch) and run beside it; it ends after it, so that whatever follows has both.
+template <typename T, int R, int K, bool REV, bool TR, bool LOCAL>
+cudaError_t launch(const SsmArgs& p, const ScanOp& op, bool beside, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(p.B * p.H * op.segments));
+  cfg.blockDim = dim3(8 * R / kRows);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, scan_kernel<T, R, K, REV, TR, LOCAL>, p, op);
+}
+// Cuts the walk into runs where `seg`, scratch for their states and decays, is given.
+template <int R, int K, bool TR>
+void cut(const SsmArgs& p, ScanOp* op, float* seg) {
+  using F = typename std::conditional<TR, double, float>::type;
   const int64_t units = p.B * p.H, k = seg ? scan_segments(units, p.T) : 1;
-  op.per = (p.T + k - 1) / k;
-  op.segments = op.per > 0 ? (p.T + op.per - 1) / op.per : 1;
-  if (op.segments > 1) {
-    using F = typename std::conditional<TR, double, float>::type;
-    op.seg_state = seg;
-    op.seg_decay = reinterpret_cast<F*>(seg) + units * op.segments * R * K;
-    scan_kernel<T, R, K, REV, TR, true><<<unsigned(units * op.segments), 4 * R, 0, s>>>(p, op);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  scan_kernel<T, R, K, REV, TR, false><<<unsigned(units * op.segments), 4 * R, 0, s>>>(p, op);
-  return cudaGetLastError();
+  op->per = (p.T + k - 1) / k;
+  op->segments = op->per > 0 ? (p.T + op->per - 1) / op->per : 1;
+  op->seg_state = seg;
+  op->seg_decay = reinterpret_cast<F*>(seg) + units * op->segments * R * K;
 }
 
 template <typename T, int N>
@@ -307,7 +340,12 @@ cudaError_t fwd(const SsmArgs& p, cudaStream_t s) {
   op.chunk_state = p.ckpt;
   op.chunk_stride = chunks_of(p.T) + 1;
   op.last = p.s_out;
-  return scan<T, kHeadP, N, false, false>(p, op, p.ckpt ? p.ckpt + p.B * p.H * (chunks_of(p.T) + 1) * kHeadP * N : nullptr, s);
+  cut<kHeadP, N, false>(p, &op, p.ckpt ? p.ckpt + p.B * p.H * (chunks_of(p.T) + 1) * kHeadP * N : nullptr);
+  if (op.segments > 1) {
+    const cudaError_t e = launch<T, kHeadP, N, false, false, true>(p, op, false, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch<T, kHeadP, N, false, false, false>(p, op, false, s);
 }
 
 // Sums over the heads of a group: with the scans' past parts Pc, Pb per head and q = x . dy,
@@ -335,6 +373,7 @@ __global__ void __launch_bounds__(256) heads_kernel(const SsmArgs p, const SsmSc
     return v;
   };
   bc = warp_sum(bc);
+#pragma unroll 4
   for (int64_t h = g * hg; h < (g + 1) * hg; ++h) {
     const float d = step_of<T>(p, bt, h);
     const float2 x2 = load2(static_cast<const T*>(p.x) + bt * p.x_ld + h * kHeadP + 2 * lane);
@@ -394,7 +433,8 @@ template <typename T, int N>
 cudaError_t bwd(const SsmArgs& p, cudaStream_t s) {
   const SsmScratch sc = ssm_scratch(p.B, p.T, p.H, p.G, N, false);
   const int64_t nc = chunks_of(p.T);
-  float* seg = p.scratch + sc.seg;
+  const int64_t run = ssm_run_floats(p.B, p.T, p.H, N);
+  float* seg = p.scratch + sc.seg;   // dx, then dc and db in fp64
   ScanOp dc{};   // forward again, transposed
   dc.rin = p.b; dc.rin_ld = p.b_ld; dc.rin_g = true;
   dc.kin = p.x; dc.kin_ld = p.x_ld;
@@ -419,10 +459,18 @@ cudaError_t bwd(const SsmArgs& p, cudaStream_t s) {
   db.init = p.dsT;
   db.out = p.scratch + sc.dbp;
   db.chunk_state = p.scratch + sc.dstate; db.chunk_stride = nc;
+  cut<kHeadP, N, false>(p, &dx, seg);
+  cut<N, kHeadP, true>(p, &dc, seg + run);
+  cut<N, kHeadP, true>(p, &db, seg + 3 * run);
   cudaError_t e;
-  if ((e = scan<T, N, kHeadP, false, true>(p, dc, seg, s)) != cudaSuccess) return e;
-  if ((e = scan<T, kHeadP, N, true, false>(p, dx, seg, s)) != cudaSuccess) return e;
-  if ((e = scan<T, N, kHeadP, true, true>(p, db, seg, s)) != cudaSuccess) return e;
+  if (dc.segments > 1) {
+    if ((e = launch<T, N, kHeadP, false, true, true>(p, dc, false, s)) != cudaSuccess) return e;
+    if ((e = launch<T, kHeadP, N, true, false, true>(p, dx, true, s)) != cudaSuccess) return e;
+    if ((e = launch<T, N, kHeadP, true, true, true>(p, db, true, s)) != cudaSuccess) return e;
+  }
+  if ((e = launch<T, N, kHeadP, false, true, false>(p, dc, false, s)) != cudaSuccess) return e;
+  if ((e = launch<T, kHeadP, N, true, false, false>(p, dx, true, s)) != cudaSuccess) return e;
+  if ((e = launch<T, N, kHeadP, true, true, false>(p, db, true, s)) != cudaSuccess) return e;
   heads_kernel<T, N><<<unsigned((p.B * p.T * p.G + 7) / 8), 256, 0, s>>>(p, sc);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   anchor_kernel<<<unsigned(p.B * p.H * nc), 256, 0, s>>>(p, sc);
@@ -445,10 +493,10 @@ cudaError_t run_dtype(const SsmArgs& p, int dtype, bool backward, cudaStream_t s
 
 }  // namespace
 
-// fp32 elements of the runs' states and decays (fp64: twice as many).
+// fp32 elements of the runs' states and decays (fp64: twice as many); whole 16 bytes, as several follow one another.
 int64_t ssm_run_floats(int64_t B, int64_t T, int64_t H, int N) {
   const int64_t k = scan_segments(B * H, T);
-  return k > 1 ? B * H * k * (kHeadP * N + 1) : 0;
+  return k > 1 ? (B * H * k * (kHeadP * N + 1) + 3) / 4 * 4 : 0;
 }
 
 cudaError_t launch_ssm_scan_fwd(const SsmArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, false, s); }

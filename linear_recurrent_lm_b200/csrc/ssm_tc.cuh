@@ -24,12 +24,8 @@ __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t mn_block_bytes)
          | (uint64_t(1024 >> 4) << 32)                                                           // distance of 8-row groups
          | (uint64_t(1) << 46) | (uint64_t(2) << 61);                                            // version, 128-byte swizzle
 }
-// Operand `step` (K = 16 each) of a K-major operand whose 64-column tiles are `tile_bytes` apart, from the descriptor of
-// its start (the address sits in the low bits, in units of 16 bytes).
-__device__ __forceinline__ uint64_t k_step(uint64_t d, int step, uint32_t tile_bytes = kTileBytes) {
-  return d + (((step >> 2) * tile_bytes + (step & 3) * 32) >> 4);
-}
-// The same of an MN-major one (K along the rows).
+// Operand `step` (K = 16 each) of an MN-major operand (K along the rows), from the descriptor of its start: the address sits
+// in the low bits, in units of 16 bytes.
 __device__ __forceinline__ uint64_t mn_step(uint64_t d, int step) { return d + ((step * 2048) >> 4); }
 
 // D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc], kind::f16
@@ -139,7 +135,7 @@ struct WarpBarrier {
 
 // ---- decays of one chunk.  Lambda_t: sum of log2 decays from the chunk's start up to and with token t, summed in fp64
 // and kept as a pair of floats; r_t: a reset at or before t in the chunk.  Everything is zero behind the row's end.
-struct Decays {
+struct alignas(16) Decays {   // (its rows are read four floats at a time, in arrays of these)
   float hi[kQ], lo[kQ];   // Lambda_t
   float d[kQ];            // step
   float in[kQ];           // 2^Lambda_t, 0 where r_t: what is left at t of the state that enters the chunk
@@ -152,7 +148,6 @@ struct Decays {
   float total;            // 2^Lambda_end, 0 with a reset
   int resets;             // any reset in the chunk
   int growing;            // any decay above one
-  int pad;
 };
 
 // 2^(Lambda_a - Lambda_b) of two tokens (or of the chunk's start: zero).
@@ -177,7 +172,8 @@ struct RawSteps {
 };
 
 // One warp fills `o` for chunk c: 32 tokens at a time, in rolled loops (see the chunk kernel on code size).
-__device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, bool backward, Decays& o) {
+__device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, bool backward,
+                                             Decays& o) {
   const int lane = threadIdx.x & 31;
   const double A2 = double(A) * 1.4426950408889634074;
   double before = 0.0;      // Lambda at the start of the block
@@ -188,7 +184,7 @@ __device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bi
     const int t = 32 * k + lane;
     const float v = (k == 0 ? raw.v[0] : k == 1 ? raw.v[1] : k == 2 ? raw.v[2] : raw.v[3]) + bias;
     const float d = c * kQ + t < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
-    double sum = double(d) * A2;
+    double sum = fmax(double(d) * A2, -1e30);   // nothing is left long before, and sums of 128 stay finite as floats
     grow |= sum > 0.0;
 #pragma unroll 1
     for (int s = 1; s < 32; s *= 2) {

@@ -127,7 +127,12 @@ wkv7_status_t check_ssm(const wkv7_desc_t* d, const wkv7_ssm_t* sp, wkv7::SsmArg
   return check_ptrs(false, {sp->A, sp->D, sp->dt_bias}, 4);
 }
 
-bool chunked(const wkv7_desc_t* d) { return d->dtype == WKV7_BF16 && d->algo != WKV7_ALGO_SCAN; }
+// AUTO: the tensor cores for bf16, but not in the forward of a few tokens, which would fill a 128-token chunk with zeros.
+// Forward, us, token order against chunks, B=8 H=32 N=64: T=8 7.8 / 20, T=16 10 / 20, T=32 16 / 20, T=64 27 / 20; N=128: 11 / 22,
+// 15 / 22, 23 / 22, 39 / 22; B=1 N=64: T=16 7.4 / 10.5, T=32 11.3 / 10.4.  Backward, B=8 H=32 N=64: T=1 52 / 46, T=128 249 / 53.
+bool chunked(const wkv7_desc_t* d, bool forward) {
+  return d->dtype == WKV7_BF16 && d->algo != WKV7_ALGO_SCAN && !(forward && d->algo == WKV7_ALGO_AUTO && d->T <= 16);
+}
 
 // ------------------------------------------------------------------ norm
 wkv7_status_t check_rms(const wkv7_desc_t* d, const wkv7_rms_t* rn, wkv7::RmsArgs* a, bool sizes_only = false) {
@@ -217,7 +222,7 @@ size_t wkv7_ssm_workspace_bytes(const wkv7_desc_t* d, const wkv7_ssm_t* sp) {
   if (check_ssm(d, sp, &a, true) != WKV7_OK || d->T == 0) return 0;
   const int64_t nc = (d->T + wkv7::kSsmChunk - 1) / wkv7::kSsmChunk;
   return size_t(d->B * d->H * (nc + 1) * wkv7::kHeadP * d->N +
-                (chunked(d) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : wkv7::ssm_run_floats(d->B, d->T, d->H, d->N))) * 4;
+                (chunked(d, true) ? wkv7::ssm_segment_floats(d->B, d->T, d->H, d->N) : wkv7::ssm_run_floats(d->B, d->T, d->H, d->N))) * 4;
 }
 
 wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const void* x, const void* dt, const void* b,
@@ -237,7 +242,7 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const
   a.x = x; a.dt = dt; a.b = b; a.c = c; a.s0 = s0; a.reset = reset; a.y = y; a.s_out = s_out;
   a.ckpt = static_cast<float*>(workspace);
   cudaError_t e;
-  if (chunked(d)) {
+  if (chunked(d, true)) {
     wkv7::stc::TileMaps tm;
     if (!wkv7::encode_ssm_maps(a, false, &tm)) return WKV7_ERR_CUDA;
     e = wkv7::launch_ssm_chunk_fwd(a, tm, s);
@@ -250,7 +255,7 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const
 size_t wkv7_ssm_scratch_bytes(const wkv7_desc_t* d, const wkv7_ssm_t* sp) {
   wkv7::SsmArgs a;
   if (check_ssm(d, sp, &a, true) != WKV7_OK || d->T == 0) return 0;
-  return size_t(wkv7::ssm_scratch(d->B, d->T, d->H, sp->G, d->N, chunked(d)).total) * 4;
+  return size_t(wkv7::ssm_scratch(d->B, d->T, d->H, sp->G, d->N, chunked(d, false)).total) * 4;
 }
 
 wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, const void* x, const void* dt, const void* b,
@@ -277,14 +282,14 @@ wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, cons
   a.dx = dx; a.ddt = ddt; a.db = db; a.dc = dc; a.dA = dA; a.dD = dD; a.ddt_bias = ddt_bias; a.ds0 = ds0;
   a.scratch = static_cast<float*>(scratch);
   cudaError_t e;
-  if (chunked(d)) {
+  if (chunked(d, false)) {
     wkv7::stc::TileMaps tm;
     if (!wkv7::encode_ssm_maps(a, true, &tm)) return WKV7_ERR_CUDA;
     e = wkv7::launch_ssm_chunk_bwd(a, tm, s);
   } else {
     e = wkv7::launch_ssm_scan_bwd(a, d->dtype, s);
   }
-  if (e == cudaSuccess) e = wkv7::launch_ssm_decay(a, d->dtype, chunked(d), s);
+  if (e == cudaSuccess) e = wkv7::launch_ssm_decay(a, d->dtype, chunked(d, false), s);
   return finish(d, e,
                 {{dx, n, d->dtype}, {ddt, units * d->T, d->dtype}, {db, nb, d->dtype}, {dc, nb, d->dtype}, {dA, d->H, WKV7_F32},
                  {dD, d->H, WKV7_F32}, {ddt_bias, d->H, WKV7_F32}, {ds0, st, WKV7_F32}},

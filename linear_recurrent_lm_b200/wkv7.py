@@ -600,7 +600,7 @@ def ssm_forward(x, dt, A, b, c, D=None, dt_bias=None, s0=None, reset=None, *, so
 
     x [B,T,H,64], dt [B,T,H], b, c [B,T,G,N] (H / G consecutive heads share a group; N = 64 or 128; token rows may be
     slices of wider ones), A, D, dt_bias fp32 [H], s0 fp32 [B,H,64,N], reset [B,T].  algo "auto" is "chunked" (tensor
-    cores) for bf16 and "scan" (token order) else; under "chunked" a NaN or infinity in a token may reach every output of
+    cores) for bf16 rows of more than 16 tokens and "scan" (token order) else; under "chunked" a NaN or infinity in a token may reach every output of
     its 128-token chunk, so fill padding with finite values.  Returns (y, s_out, workspace)."""
     d, sp, ptrs, (B, T, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 2, algo, flags)
     y = _out(y, "y", (B, T, H, N_HEAD), x.dtype, x)

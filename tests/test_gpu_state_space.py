@@ -355,6 +355,16 @@ def test_ssm_masked_steps(W, dtype, algo):
         assert not g[n][:, 100:].any() and not g[n][1, 40:60].any(), n
 
 
+@pytest.mark.parametrize("dtype,algo", FORMS)
+def test_ssm_decays_beyond_the_exponents_range(W, dtype, algo):
+    """d A overflows fp32: nothing is remembered, and nothing is NaN."""
+    rng = np.random.default_rng(255)
+    dev, ref = _ssm_case(rng, dtype, 2, 140, 4, 1, 64)
+    dev["dt_bias"], ref["dt_bias"] = _dev(np.full(4, 100.0, np.float32))
+    dev["A"], ref["A"] = _dev(np.array([-3e38, -1e37, -1e30, -3e38], np.float32))
+    _ssm_check(W, rng, dtype, algo, dev, ref)
+
+
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("T", (90, 700))
 def test_ssm_scan_keeps_what_is_not_finite_in_its_segment(W, dtype, T):
