@@ -141,10 +141,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
     if (first < n) raw.load(p, b, h, chunk(first));
     for (int i = first; i < n; i += kDecayWarps) {
       if (i >= 3 && !wait.warp(&tl.dec_free[i % 3], ph3(i - 3))) break;
-      chunk_decays(p, A, bias, chunk(i), raw, false, tl.dec[i % 3]);
+      const RawSteps now = raw;
+      if (i + kDecayWarps < n) raw.load(p, b, h, chunk(i + kDecayWarps));
+      chunk_decays<OUT ? kForward : REV ? kReversed : kStates>(p, A, bias, chunk(i), now, tl.dec[i % 3]);
       __syncwarp();
       if (lane == 0) arrive(&tl.dec_full[i % 3]);
-      if (i + kDecayWarps < n) raw.load(p, b, h, chunk(i + kDecayWarps));
     }
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue

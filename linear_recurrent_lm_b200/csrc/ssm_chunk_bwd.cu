@@ -196,10 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
     for (int i = 0; i < n; ++i) {
       const float A = __ldg(p.A + h0 + i), bias = p.dt_bias ? __ldg(p.dt_bias + h0 + i) : 0.f;
       if (i >= 3 && !wait.warp(&tl.dec_free[i % 3], unsigned(i / 3 - 1) & 1u)) break;
-      chunk_decays(p, A, bias, c, raw, true, tl.dec[i % 3]);
+      const RawSteps now = raw;
+      if (i + 1 < n) raw.load(p, b, h0 + i + 1, c);
+      chunk_decays<kBackward>(p, A, bias, c, now, tl.dec[i % 3]);
       __syncwarp();
       if (lane == 0) arrive(&tl.dec_full[i % 3]);
-      if (i + 1 < n) raw.load(p, b, h0 + i + 1, c);
     }
   } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issue: one elected lane of a warp that stays together

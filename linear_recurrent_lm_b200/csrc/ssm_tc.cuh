@@ -155,67 +155,100 @@ __device__ __forceinline__ float decay_between(float ahi, float alo, float bhi, 
   return ex2_pair(ahi - bhi, alo - blo);
 }
 
-// The raw steps and resets of tokens 32 k + lane of chunk c (loads only, so that they can be under way early).
+// The raw steps and resets of tokens 4 lane + k of chunk c (loads only, so that they can be under way early).
 struct RawSteps {
   float v[4];
   unsigned rst;   // bit k
   __device__ __forceinline__ void load(const SsmArgs& p, int64_t b, int64_t h, int64_t c) {
-    const int64_t t0 = c * kQ + (threadIdx.x & 31), bt = b * p.T + t0;
+    const int64_t t0 = c * kQ + 4 * (threadIdx.x & 31), bt = b * p.T + t0;
     rst = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const bool ok = t0 + 32 * k < p.T;
-      v[k] = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dt)[(bt + 32 * k) * p.dt_ld + h]) : 0.f;
-      if (ok && p.reset && p.reset[bt + 32 * k]) rst |= 1u << k;
+      const bool ok = t0 + k < p.T;
+      v[k] = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dt)[(bt + k) * p.dt_ld + h]) : 0.f;
+      if (ok && p.reset && p.reset[bt + k]) rst |= 1u << k;
     }
   }
 };
 
-// One warp fills `o` for chunk c: 32 tokens at a time, in rolled loops (see the chunk kernel on code size).
-__device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, bool backward,
-                                             Decays& o) {
+// Who reads the decays: the forward, the backward, or a pass over the states alone (forward or reversed).
+enum Reader { kForward, kBackward, kStates, kReversed };
+
+// One warp fills `o` for chunk c, four tokens per lane: their chains overlap, and one scan over the lanes serves all 128
+// tokens (32 tokens at a time took 7000 cycles, which bounded the reversed state pass: 194 us for B=8 T=4096 H=32 N=128).
+template <int READER>
+__device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, Decays& o) {
   const int lane = threadIdx.x & 31;
+  const int64_t t0 = c * kQ + 4 * lane;
   const double A2 = double(A) * 1.4426950408889634074;
-  double before = 0.0;      // Lambda at the start of the block
-  int last = -1;            // last reset before the block
+  float d[4];
+  double l[4], sum = 0.0;
+  int st[4], last = -1;
   bool grow = false;
-#pragma unroll 1
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int t = 32 * k + lane;
-    const float v = (k == 0 ? raw.v[0] : k == 1 ? raw.v[1] : k == 2 ? raw.v[2] : raw.v[3]) + bias;
-    const float d = c * kQ + t < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
-    double sum = fmax(double(d) * A2, -1e30);   // nothing is left long before, and sums of 128 stay finite as floats
-    grow |= sum > 0.0;
-#pragma unroll 1
-    for (int s = 1; s < 32; s *= 2) {
-      const double u = __shfl_up_sync(0xffffffffu, sum, s);
-      if (lane >= s) sum += u;
-    }
-    const double l = before + sum;
-    const unsigned rst = __ballot_sync(0xffffffffu, raw.rst >> k & 1u), upto = rst & (0xffffffffu >> (31 - lane));
-    const int prev = upto ? 32 * k + 31 - __clz(upto) : last;
-    const float hi = float(l), lo = float(l - double(hi));
-    o.hi[t] = hi;
-    o.lo[t] = lo;
-    o.d[t] = d;
-    o.rel[t] = float(sum);
-    o.in[t] = prev < 0 ? ex2_pair(hi, lo) : 0.f;
-    o.start[t] = prev < 0 ? 0 : prev;
-    before = __shfl_sync(0xffffffffu, l, 31);
-    if (rst) last = 32 * k + 31 - __clz(rst);
+    const float v = raw.v[k] + bias;
+    d[k] = t0 + k < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
+    const double x = fmax(double(d[k]) * A2, -1e30);   // nothing is left long before, and sums of 128 stay finite as floats
+    grow |= x > 0.0;
+    sum += x;
+    l[k] = sum;
+    if (raw.rst >> k & 1u) last = 4 * lane + k;
+    st[k] = last;
   }
-  const float ehi = float(before), elo = float(before - double(ehi));
-  __syncwarp();
-#pragma unroll 1
-  for (int t = lane; t < kQ; t += 32) o.out[t] = t >= last ? decay_between(ehi, elo, o.hi[t], o.lo[t]) : 0.f;
-#pragma unroll 1
-  for (int k = 0; k < 6; ++k) {
-    if (!backward) {
-      const int w = k < 1 ? 1 : k < 3 ? 2 : 3, t = 32 * (k - w * (w - 1) / 2) + lane, m = 32 * w - 1;
-      o.far[32 * k + lane] = o.d[t] * decay_between(o.hi[m], o.lo[m], o.hi[t], o.lo[t]);
-    } else {
-      const int w = k < 3 ? 0 : k < 5 ? 1 : 2, t = 32 * (k < 3 ? k + 1 : k < 5 ? k - 1 : 3) + lane, m = 32 * w + 31;
-      o.far[32 * k + lane] = decay_between(o.hi[t], o.lo[t], o.hi[m], o.lo[m]);
+#pragma unroll
+  for (int s = 1; s < 32; s *= 2) {
+    const double u = __shfl_up_sync(0xffffffffu, sum, s);
+    const int m = __shfl_up_sync(0xffffffffu, last, s);
+    if (lane >= s) {
+      sum += u;
+      last = m > last ? m : last;
+    }
+  }
+  double ex = __shfl_up_sync(0xffffffffu, sum, 1);   // Lambda and the last reset before this lane's tokens
+  int before = __shfl_up_sync(0xffffffffu, last, 1);
+  if (lane == 0) {
+    ex = 0.0;
+    before = -1;
+  }
+  const double block = __shfl_sync(0xffffffffu, ex, lane & 24), end = __shfl_sync(0xffffffffu, sum, 31);
+  last = __shfl_sync(0xffffffffu, last, 31);
+  const float ehi = float(end), elo = float(end - double(ehi));
+  float hi[4], lo[4], rel[4], in[4], out[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    l[k] += ex;
+    hi[k] = float(l[k]);
+    lo[k] = float(l[k] - double(hi[k]));
+    rel[k] = float(l[k] - block);
+    st[k] = st[k] < 0 ? before : st[k];
+    in[k] = st[k] < 0 ? ex2_pair(hi[k], lo[k]) : 0.f;
+    if (READER != kReversed) out[k] = 4 * lane + k >= last ? decay_between(ehi, elo, hi[k], lo[k]) : 0.f;
+    st[k] = st[k] < 0 ? 0 : st[k];
+  }
+  auto put = [&](float* dst, const float (&v)[4]) { *reinterpret_cast<float4*>(dst + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]); };
+  if (READER != kReversed) {
+    put(o.d, d);
+    put(o.out, out);
+  }
+  if (READER != kStates) put(o.in, in);
+  if (READER == kForward || READER == kBackward) {
+    put(o.hi, hi);
+    put(o.lo, lo);
+    put(o.rel, rel);
+    *reinterpret_cast<int4*>(o.start + 4 * lane) = make_int4(st[0], st[1], st[2], st[3]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) {   // relative to token 32 j - 1: the start of row block j, the end of row block j - 1
+      const float mh = __shfl_sync(0xffffffffu, hi[3], 8 * j - 1), ml = __shfl_sync(0xffffffffu, lo[3], 8 * j - 1);
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = READER == kForward ? d[k] * decay_between(mh, ml, hi[k], lo[k]) : decay_between(hi[k], lo[k], mh, ml);
+      if (READER == kForward) {
+        if (lane < 8 * j) put(o.far + 16 * j * (j - 1), v);
+      } else if (lane >= 8 * j) {
+        put(o.far + (j == 1 ? 0 : j == 2 ? 96 : 160) - 32 * j, v);
+      }
     }
   }
   const unsigned any_grow = __ballot_sync(0xffffffffu, grow);

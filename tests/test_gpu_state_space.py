@@ -691,6 +691,35 @@ def test_two_graphs_share_no_scratch(W):
             assert all(torch.equal(out[n], ref[n]) for n in ref)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T", (40, 400))
+def test_token_order_in_a_graph(W, dtype, T):
+    """The token-order backward's scans run beside one another: captured and replayed back to back with another call
+    behind them on the stream, they give the eager bits every time."""
+    import torch
+    rng = np.random.default_rng(285)
+    dev, _ = _ssm_case(rng, dtype, 2, T, 6, 2, 128, strided=False)
+    dy = torch.randn(2, T, 6, 64, device="cuda").to(_t(dtype))
+
+    def run():
+        y, s, ws = W.ssm_forward(**dev, algo="scan")
+        g = W.ssm_backward(dy=dy, workspace=ws, algo="scan", **dev)
+        y2, _, _ = W.ssm_forward(g["dx"], dev["dt"], dev["A"], g["db"], g["dc"], algo="scan")   # reads what came before
+        return {"y": y, "s": s, "y2": y2, **g}
+    ref = {n: t.clone() for n, t in run().items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for _ in range(3):
+        for _ in range(10):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n], ref[n]) for n in ref)
+        again = run()
+        assert all(torch.equal(again[n], ref[n]) for n in ref)
+
+
 def test_finite_check_reports(W):
     import torch
     x = torch.randn(4, 256, device="cuda").bfloat16()
