@@ -220,10 +220,16 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
       st8(lanes + kTM + 16 * r + 8, zero);
       tc::wait_st();
     }
-    auto put = [&](float* dst) {   // [64][N]
+    auto put = [&](float* dst, int q0 = 0, int q1 = 16) {   // [64][N]
       if (mine)
 #pragma unroll
-        for (int q = 0; q < 16; ++q) dst[at + q * N] = S[q];
+        for (int q = 0; q < 16; ++q)
+          if (q >= q0 && q < q1) dst[at + q * N] = S[q];
+    };
+    // The state that enters chunk e, four of a thread's sixteen rows at a time: its stores are spread over the phases, as
+    // they would fill the store queue at once (256 of 128 bytes per CTA).
+    auto put_part = [&](int e, int k) {
+      if (op.states) put(op.states + (unit * op.stride + chunk(e)) * 64 * N, 4 * k, 4 * k + 4);
     };
     // The weighted x of chunk e in three bf16 parts (its buffer has been read).  The smallest part first: the tensor core
     // cuts its sums off below their leading bits, which the large part then meets in its own eight steps only.
@@ -322,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) arrive(&tl.m_ready[i & 1]);
+          put_part(i, 3);
         }
         if (SM::kXSets == 2 && i + 1 < n && !(ok = weigh(i + 1))) break;   // (U(i - 1) has read that buffer)
         // ---- S(i + 1) = e^{Lambda_end} S(i) + U(i)
@@ -359,9 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           tc::fence_smem_to_async();
           __syncwarp();
           if (lane == 0) arrive(&tl.sh_ready[e & 1]);
+          put_part(e, 0);
+        } else if (op.states) {
+          put(op.states + (unit * op.stride + chunk(e)) * 64 * N);
         }
-        if (op.states) put(op.states + (unit * op.stride + chunk(e)) * 64 * N);
-        if (SM::kXSets == 1 && !(ok = weigh(e))) break;   // (U(i) has read its parts)
       }
       if (OUT && i >= 0) {
         // ---- Y(i) = Y1 + in Y2 + (D + M_tt) x
@@ -393,6 +401,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         __syncwarp();
         if (lane == 0) arrive(&tl.x_free[i & 1]);
       }
+      // (U(i) has read its parts.  Behind Y(i), which frees a buffer of x for the loader two chunks ahead.)
+      if (OUT && e < n) put_part(e, 1);
+      if (SM::kXSets == 1 && e < n && !(ok = weigh(e))) break;
+      if (OUT && e < n) put_part(e, 2);
     }
     if (ok) {
       if (op.local) {

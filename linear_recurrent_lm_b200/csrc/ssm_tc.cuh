@@ -157,16 +157,15 @@ __device__ __forceinline__ float decay_between(float ahi, float alo, float bhi, 
 
 // The raw steps and resets of tokens 4 lane + k of chunk c (loads only, so that they can be under way early).
 struct RawSteps {
-  float v[4];
-  unsigned rst;   // bit k
+  unsigned short v[4];   // bf16 as loaded: a conversion here would wait for the load
+  uint8_t rst[4];
   __device__ __forceinline__ void load(const SsmArgs& p, int64_t b, int64_t h, int64_t c) {
     const int64_t t0 = c * kQ + 4 * (threadIdx.x & 31), bt = b * p.T + t0;
-    rst = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool ok = t0 + k < p.T;
-      v[k] = ok ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.dt)[(bt + k) * p.dt_ld + h]) : 0.f;
-      if (ok && p.reset && p.reset[bt + k]) rst |= 1u << k;
+      v[k] = ok ? static_cast<const unsigned short*>(p.dt)[(bt + k) * p.dt_ld + h] : 0;
+      rst[k] = ok && p.reset ? p.reset[bt + k] : 0;
     }
   }
 };
@@ -187,13 +186,13 @@ __device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bi
   bool grow = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float v = raw.v[k] + bias;
+    const float v = __uint_as_float(unsigned(raw.v[k]) << 16) + bias;
     d[k] = t0 + k < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
     const double x = fmax(double(d[k]) * A2, -1e30);   // nothing is left long before, and sums of 128 stay finite as floats
     grow |= x > 0.0;
     sum += x;
     l[k] = sum;
-    if (raw.rst >> k & 1u) last = 4 * lane + k;
+    if (raw.rst[k]) last = 4 * lane + k;
     st[k] = last;
   }
 #pragma unroll
