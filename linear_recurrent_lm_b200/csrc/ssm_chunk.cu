@@ -18,16 +18,16 @@
 //         factor, both relative to the row block's start (so at most one), which leaves 32 exponentials per row, not 128
 //   S     thread = state column, 16 fp32 rows of it in registers: add U, and write the bf16 parts for C S^T
 //   XS    thread = token row, a quarter of it: the weighted x in three bf16 parts
-//   Y     thread = token row, a quarter of it: Y1 + in Y2 + (D + M_tt) x, stored as whole 32-byte sectors
-// while warp 16 issues the MMAs (one phase ahead of what is read), warp 17 loads tiles (TMA, 128-byte swizzle) and
+//   Y     thread = token row, a quarter of it: Y1 + in Y2 + (D + M_tt) x, in the place of x
+// while warp 16 issues the MMAs (one phase ahead of what is read), warp 17 loads tiles and stores y (TMA, 128-byte swizzle) and
 // warps 18 and 19 prepare the decays (fp64 prefix sums), every other chunk each, up to three ahead.
 //
 // What bounds it: instruction fetch.  Code beyond the few KB of a scheduler's own cache arrives at 5.5 cycles per
 // instruction (measured on straight-line FMAs), once for all warps of the scheduler that run it together.  Roles on
 // separate warps (M, state, XS) therefore ran at 7300 to 11600 cycles per chunk; all warps in the same phase, loops rolled,
-// share the fetches: about 7000.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes
+// share the fetches: about 6500.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes
 // (a product of 64 columns with A in shared memory is bound by reading it): G 512, C S^T 784, M X 260, state 1176.
-// B=8 T=4096 H=32 N=128: 290 us (256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed state pass 194 us.
+// B=8 T=4096 H=32 N=128: 242 us (256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed state pass 140 us.
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -114,7 +114,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
     if (lane == 0) {
       const CUtensorMap* mx = REV ? &tm.dy : &tm.x;
       const CUtensorMap* mb = REV ? &tm.c : &tm.b;
+      // y of a chunk takes the place of its x (each thread that writes 16 channels of a row there has read those of x), and
+      // goes out as a tile: as two 16-byte stores per row and thread it took 1800 cycles of the store path per chunk.
+      auto store_y = [&](int i) {
+        if (!wait(&tl.x_free[i & 1], ph(i))) return false;
+        tma_store_4d(&tm.y, sm + SM::kX + (i & 1) * kTileBytes, 0, int(h), int(chunk(i) * kQ), int(b));
+        tma_store_read();
+        return true;
+      };
+      bool ok = true;
       for (int i = 0; i < n; ++i) {
+        ok = false;
         const int t0 = int(chunk(i) * kQ), s = i & 1;
         if (i >= 2 && !wait(&tl.u_full[s], ph(i - 2))) break;
         mbar_arrive_expect_tx(&tl.b_full[s], NB * kTileBytes);
@@ -127,10 +137,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           for (int j = 0; j < NB; ++j) tma_load_4d(sm + SM::kC + j * kTileBytes, &tm.c, 64 * j, int(g), t0, int(b), &tl.c_full);
           ++c_loads;
         }
-        if (i >= 2 && !wait(&tl.x_free[s], ph(i - 2))) break;
+        if (i >= 2 && !(OUT ? store_y(i - 2) : wait(&tl.x_free[s], ph(i - 2)))) break;
         mbar_arrive_expect_tx(&tl.x_full[s], kTileBytes);
         tma_load_4d(sm + SM::kX + s * kTileBytes, mx, 0, int(h), t0, int(b), &tl.x_full[s]);
         ++x_loads;
+        ok = true;
+      }
+      if (OUT) {
+        for (int i = n >= 2 ? n - 2 : 0; ok && i < n; ++i) ok = store_y(i);
+        tma_store_done();
       }
     }
   } else if (warp >= 18) {
@@ -383,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         tc::fence_before_sync();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(sm + SM::kX + (i & 1) * kTileBytes + swz(row, 2 * r + j));
+          uint4* tile = reinterpret_cast<uint4*>(sm + SM::kX + (i & 1) * kTileBytes + swz(row, 2 * r + j));
+          const uint4 xv = *tile;
           const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
           uint32_t o[4];
 #pragma unroll
@@ -393,13 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
             const float2 y = fma2(make_float2(dx, dx), stc::unpack(xi[k]), f);
             o[k] = pack(y.x, y.y);
           }
-          const int64_t t = chunk(i) * kQ + row;
-          if (t < p.T && range_ok(t, 1, p.T, p.status))
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.y) + ((b * p.T + t) * p.H + h) * 64 + 16 * r + 8 * j) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+          *tile = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        tc::fence_smem_to_async();
         __syncwarp();
-        if (lane == 0) arrive(&tl.x_free[i & 1]);
+        if (lane == 0) arrive(&tl.x_free[i & 1]);   // (to the loader: y is there)
       }
       // (U(i) has read its parts.  Behind Y(i), which frees a buffer of x for the loader two chunks ahead.)
       if (OUT && e < n) put_part(e, 1);

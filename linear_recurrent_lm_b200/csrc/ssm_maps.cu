@@ -44,7 +44,7 @@ bool encode_ssm_maps(const SsmArgs& p, bool backward, stc::TileMaps* tm) {
   if (!enc) return false;
   const bool ok = encode(enc, p, p.x, kHeadP, p.H, p.x_ld, &tm->x) && encode(enc, p, p.b, p.N, p.G, p.b_ld, &tm->b) &&
             encode(enc, p, p.c, p.N, p.G, p.c_ld, &tm->c);
-  return ok && (!backward || encode(enc, p, p.dy, kHeadP, p.H, p.H * kHeadP, &tm->dy));
+  return ok && encode(enc, p, backward ? p.dy : p.y, kHeadP, p.H, p.H * kHeadP, backward ? &tm->dy : &tm->y);
 }
 
 }  // namespace wkv7

@@ -118,8 +118,17 @@ __device__ __forceinline__ void arrive(unsigned long long* bar) {
 
 // ---- token tiles by TMA: {64, heads or groups, T, B}, box {64, 1, 128, 1}; tokens past T read as zeros
 struct TileMaps {
-  CUtensorMap x, b, c, dy;
+  CUtensorMap x, b, c, dy, y;   // dy: backward; y, written: forward
 };
+// A tile back to global memory (rows past T are left out), and the wait until it has been read, or written.
+__device__ __forceinline__ void tma_store_4d(const void* map, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(
+                   reinterpret_cast<unsigned long long>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // A barrier of `n` warps that gives up with everyone else: each use toggles the phase.
 struct WarpBarrier {
   unsigned long long* bar;
@@ -174,7 +183,8 @@ struct RawSteps {
 enum Reader { kForward, kBackward, kStates, kReversed };
 
 // One warp fills `o` for chunk c, four tokens per lane: their chains overlap, and one scan over the lanes serves all 128
-// tokens (32 tokens at a time took 7000 cycles, which bounded the reversed state pass: 194 us for B=8 T=4096 H=32 N=128).
+// tokens (32 tokens at a time took 7000 cycles, which bounded the reversed state pass: 194 us for B=8 T=4096 H=32 N=128,
+// now 140).
 template <int READER>
 __device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bias, int64_t c, const RawSteps& raw, Decays& o) {
   const int lane = threadIdx.x & 31;
