@@ -469,7 +469,7 @@ cudaError_t run_n(const SsmArgs& p, const TileMaps& tm, const ChunkOp& op, cudaS
 
 // Runs that a row's chunks are cut into: with fewer rows of heads than SMs, as many as fill them, of at least 2 chunks.  A
 // cut row is walked twice, first for the state that each run leaves (without the outputs' work), then from it on, so it
-// takes three runs to gain.  B=1 H=32 N=128: T=1024 32 us against 40 whole, T=2048 44 against 71, T=4096 72 against 132.
+// takes three runs to gain.  B=1 H=32 N=128: T=1024 28 us against 34 whole, T=2048 38 against 58, T=4096 57 against 106.
 int64_t ssm_segments(int64_t units, int64_t nc) {
   const int64_t fit = units > 0 ? 148 / units : 1, most = nc / 2, k = fit < most ? fit : most;
   return k >= 3 ? k : 1;
