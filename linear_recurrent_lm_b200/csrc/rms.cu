@@ -9,8 +9,8 @@
 // threads (1, 2 or 4 16-byte vectors each), so both reductions and the outputs come from one
 // read.  Up to 32 threads reduce by shuffles alone; wider slices add one pass through shared memory.  Short
 // slices share a CTA of 128 threads; CTAs are that small so that several independent ones per SM cover each other's
-// reductions.  Measured for bf16, 67 M elements, slices of 2048: forward with residual 86 us (6.2 TB/s), plain 55 us (4.8),
-// backward 91 us (4.4); slices of 8192 3.8 to 4.8 TB/s, of 16384 3.2 to 4.2.
+// reductions.  Measured for bf16, 67 M elements, slices of 2048: forward with residual 86 us (6.2 TB/s), plain 55 us (4.9),
+// backward 85 us (4.7); slices of 64 48 us; slices of 8192 3.8 to 4.8 TB/s, of 16384 3.2 to 4.2.
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -63,6 +63,11 @@ __device__ __forceinline__ Pair slice_reduce(Pair v, int tps, float (*sm)[2]) {
 template <typename T, int VPT>
 constexpr int kMaxThreads = VPT == 1 ? kCta : VPT == 2 ? 512 : 16384 / Vec16<T>::n / 4;
 
+// Two neighbouring values of an array, for the packed fp32 instructions: the kernels are close to bound by their issue.
+template <int V>
+__device__ __forceinline__ float2& two(float (&a)[V], int e) { return *reinterpret_cast<float2*>(&a[e]); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 struct Shape {
   int64_t L, slices;   // channels of a slice; rows * groups
   int tps, spc;        // threads per slice, slices per CTA: with several, a slice has a power of two
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
       }
     }
     float h[VPT][V];
-    float ss = 0.f;
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (act[i]) {
@@ -115,8 +120,9 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
           float z[V];
           VT::get(rz[i], z);
 #pragma unroll
-          for (int e = 0; e < V; ++e)
-            h[i][e] = MODE == kResidual ? h[i][e] + z[e] : h[i][e] * (z[e] * sigmoid_of<T>(z[e]));
+          for (int e = 0; e < V; e += 2)
+            two(h[i], e) = MODE == kResidual ? add2(two(h[i], e), two(z, e))
+                                             : mul2(two(h[i], e), mul2(two(z, e), make_float2(sigmoid_of<T>(z[e]), sigmoid_of<T>(z[e + 1]))));
           if (MODE == kResidual) {   // the stored sum is normalised, so that the backward, which reads it, sees the same h
             rx[i] = VT::pack(h[i]);
             VT::get(rx[i], h[i]);
@@ -128,9 +134,9 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
         for (int e = 0; e < V; ++e) h[i][e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+      for (int e = 0; e < V; e += 2) s2 = fma2(two(h[i], e), two(h[i], e), s2);
     }
-    const float rstd = rsqrtf(fmaf(slice_reduce<false, 1>(Pair{ss, 0.f}, s.tps, sm).a, s.inv_l, p.eps));
+    const float rstd = rsqrtf(fmaf(slice_reduce<false, 1>(Pair{s2.x + s2.y, 0.f}, s.tps, sm).a, s.inv_l, p.eps));
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -140,8 +146,8 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
 #pragma unroll
         for (int u = 0; u < V / 4; ++u) {
           const float4 w4 = __ldg(w + u);
-          h[i][4 * u] *= rstd * w4.x; h[i][4 * u + 1] *= rstd * w4.y;
-          h[i][4 * u + 2] *= rstd * w4.z; h[i][4 * u + 3] *= rstd * w4.w;
+          two(h[i], 4 * u) = mul2(two(h[i], 4 * u), mul2(both(rstd), make_float2(w4.x, w4.y)));
+          two(h[i], 4 * u + 2) = mul2(two(h[i], 4 * u + 2), mul2(both(rstd), make_float2(w4.z, w4.w)));
         }
         if (QUANT == 0) VT::store(static_cast<T*>(p.out) + base + v * V, h[i]);
       }
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
           if (act[i]) {
             float q[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
+            for (int e = 0; e < V; e += 2) two(q, e) = mul2(two(h[i], e), both(inv));
             store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + v * V, q);
             if ((lane & (128 / V - 1)) == 0) p.scale[(base + v * V) >> 7] = sc;
           }
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
         if (act[i]) {
           float q[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) q[e] = h[i][e] * inv;
+          for (int e = 0; e < V; e += 2) two(q, e) = mul2(two(h[i], e), both(inv));
           store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + (i * s.tps + lane) * V, q);
         }
       if (lane == 0 && slice < s.slices) p.scale[slice] = sc;
@@ -209,7 +215,7 @@ rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
   if (HOLD)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) weight_of(i, held[HOLD ? i : 0]);
-  // The next row's loads are under way while this one is reduced (bf16, 67 M elements, slices of 2048: 92 us, 118 without),
+  // The next row's loads are under way while this one is reduced (bf16, 67 M elements, slices of 2048: 85 us, 118 without),
   // except with four vectors, which take too many registers.
   constexpr bool AHEAD = VPT < 4;
   typename VT::R nx[VPT], nz[VPT], ng[VPT];
@@ -242,7 +248,7 @@ rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
       rz[i] = nz[i];
     }
     if (AHEAD) fetch(row + nb * s.spc);
-    float ss = 0.f, gh = 0.f;
+    float2 ss = make_float2(0.f, 0.f), gh = ss;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (act[i]) {
@@ -252,13 +258,14 @@ rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
         if (!HOLD) weight_of(i, wt);
         if (GATE) VT::get(rz[i], z);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float h = GATE ? x[e] * (z[e] * sigmoid_of<T>(z[e])) : x[e];
-          ss = fmaf(h, h, ss);
-          gh = fmaf(d[e] * (HOLD ? held[HOLD ? i : 0][e] : wt[e]), h, gh);
+        for (int e = 0; e < V; e += 2) {
+          float2 h = two(x, e);
+          if (GATE) h = mul2(h, mul2(two(z, e), make_float2(sigmoid_of<T>(z[e]), sigmoid_of<T>(z[e + 1]))));
+          ss = fma2(h, h, ss);
+          gh = fma2(mul2(two(d, e), HOLD ? two(held[HOLD ? i : 0], e) : two(wt, e)), h, gh);
         }
       }
-    const Pair r = slice_reduce<false, 2>(Pair{ss, gh}, s.tps, sm);
+    const Pair r = slice_reduce<false, 2>(Pair{ss.x + ss.y, gh.x + gh.y}, s.tps, sm);
     const float rstd = rsqrtf(fmaf(r.a, s.inv_l, p.eps));
     const float m = r.b * rstd * rstd * s.inv_l;   // mean(g xhat) rstd: dh = rstd (g - h m)
 #pragma unroll
@@ -271,16 +278,22 @@ rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
         VT::get(rg[i], d);
         if (GATE || p.dh) VT::get(rz[i], z);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float sg = GATE ? sigmoid_of<T>(z[e]) : 0.f;
-          const float h = GATE ? x[e] * (z[e] * sg) : x[e];
-          dw[i][e] = fmaf(d[e], h * rstd, dw[i][e]);
-          float dh = rstd * (d[e] * (HOLD ? held[HOLD ? i : 0][e] : wt[e]) - h * m);
+        for (int e = 0; e < V; e += 2) {
+          const float2 x2 = two(x, e), d2 = two(d, e);
+          float2 h = x2, sg = make_float2(0.f, 0.f), sz = sg;
           if (GATE) {
-            dx[e] = dh * (z[e] * sg);
-            dz[e] = dh * x[e] * (sg * fmaf(z[e], 1.f - sg, 1.f));
+            sg = make_float2(sigmoid_of<T>(z[e]), sigmoid_of<T>(z[e + 1]));
+            sz = mul2(two(z, e), sg);
+            h = mul2(x2, sz);
+          }
+          two(dw[i], e) = fma2(d2, mul2(h, both(rstd)), two(dw[i], e));
+          const float2 gw = mul2(d2, HOLD ? two(held[HOLD ? i : 0], e) : two(wt, e));
+          const float2 dh = mul2(both(rstd), fma2(h, both(-m), gw));
+          if (GATE) {
+            two(dx, e) = mul2(dh, sz);
+            two(dz, e) = mul2(mul2(dh, x2), mul2(sg, fma2(two(z, e), sub2(both(1.f), sg), both(1.f))));
           } else {
-            dx[e] = p.dh ? dh + z[e] : dh;
+            two(dx, e) = p.dh ? add2(dh, two(z, e)) : dh;
           }
         }
         VT::store(static_cast<T*>(p.dx) + o, dx);
