@@ -42,8 +42,10 @@ template <int N, bool OUT>
 struct Smem {
   static constexpr int kNB = N / 64;             // 64-column tiles of b and c
   static constexpr int kX = 0, kB = kX + 2 * kTileBytes, kC = kB + 2 * kNB * kTileBytes;
-  // the parts of the weighted x twice where they fit: then those of the next chunk are made while this one's product runs
-  static constexpr int kXSets = OUT && N == 128 ? 1 : 2;
+  // The parts of the weighted x: twice for the states alone, where those of the next chunk are made while this one's product
+  // runs.  With the outputs' work once, behind Y, whose buffer of x is then free sooner (N = 64, B=8 T=4096 H=32: 213 us, 261
+  // with two).
+  static constexpr int kXSets = OUT ? 1 : 2;
   static constexpr int kXS = kC + (OUT ? kNB * kTileBytes : 0), kSH = kXS + kXSets * 3 * kTileBytes;
   static constexpr int kEnd = kSH + (OUT ? 2 * N * 128 : 0);
   struct Tail {
