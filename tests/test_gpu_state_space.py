@@ -438,7 +438,8 @@ def test_ssm_repeats_bit_for_bit(W, algo):
 # ------------------------------------------------------------------ norm
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("kind", ("plain", "residual", "gate"))
-@pytest.mark.parametrize("rows,D,groups", ((1, 8, 1), (5, 64, 8), (300, 520, 1), (3, 2048, 1), (7, 4096, 2), (2, 16384, 1), (257, 192, 3)))
+@pytest.mark.parametrize("rows,D,groups", ((1, 8, 1), (5, 64, 8), (300, 520, 1), (3, 2048, 1), (7, 4096, 2), (2, 16384, 1), (257, 192, 3),
+                                             (9, 2560, 1), (5, 15360, 3), (3, 12288, 1), (700, 1288, 1)))
 def test_rms_forward_backward(W, dtype, kind, rows, D, groups):
     rng = np.random.default_rng(300 + D)
     eps = 1e-5
@@ -465,7 +466,8 @@ def test_rms_forward_backward(W, dtype, kind, rows, D, groups):
 
 
 @pytest.mark.parametrize("dtype", DT)
-@pytest.mark.parametrize("block,D,groups", ((128, 128, 1), (128, 2048, 1), (128, 768, 2), (128, 16384, 1), (-1, 8, 1), (-1, 520, 1), (-1, 512, 8)))
+@pytest.mark.parametrize("block,D,groups", ((128, 128, 1), (128, 2048, 1), (128, 768, 2), (128, 16384, 1), (-1, 8, 1), (-1, 520, 1), (-1, 512, 8),
+                                            (128, 2560, 1), (-1, 2568, 1), (128, 10240, 2)))
 def test_rms_e4m3(W, dtype, block, D, groups):
     """Codes times scale against the norm: half a step of e4m3 (2^-4 of the value, and 2^-10 of the scale below its
     normal range), the scale exactly the largest value over 448."""
