@@ -8,8 +8,9 @@
 // kernel serves both (REV), without the outputs (OUT = false).
 //
 // Precision: x, b, c enter the products as the bf16 they are; accumulators, decays and the carried state are fp32
-// (Lambda fp64).  What is rounded: M off its diagonal to bf16 (2^-9, like y itself); S as two bf16 parts in C S^T
-// (2^-17); the weighted x as three parts in the state's update (2^-25), so that states are fp32 results.
+// (Lambda fp64).  What is rounded: M off its diagonal to two bf16 parts (2^-18; one part alone put 2^-9 of every term into y,
+// as much again as its own rounding) and S to two in C S^T (2^-18); the weighted x to three in the state's update (2^-26),
+// so that states are fp32 results.
 //
 // One CTA per (b, h) and segment of its chunks, one CTA per SM (its tiles fill the shared memory).  Sixteen warps work,
 // four per quadrant of TMEM lanes, all through the same phases of a chunk:
@@ -26,8 +27,9 @@
 // instruction (measured on straight-line FMAs), once for all warps of the scheduler that run it together.  Roles on
 // separate warps (M, state, XS) therefore ran at 7300 to 11600 cycles per chunk; all warps in the same phase, loops rolled,
 // share the fetches: about 6500.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes
-// (a product of 64 columns with A in shared memory is bound by reading it): G 512, C S^T 784, M X 260, state 1176.
-// B=8 T=4096 H=32 N=128: 242 us (256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed state pass 140 us.
+// (a product of 64 columns with A in shared memory is bound by reading it): G 512, C S^T 784, M X 520, state 1176.
+// B=8 T=4096 H=32 N=128: 240 us (219 with M in one part; 256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed
+// state pass 140 us.
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -43,8 +45,8 @@ struct Smem {
   static constexpr int kNB = N / 64;             // 64-column tiles of b and c
   static constexpr int kX = 0, kB = kX + 2 * kTileBytes, kC = kB + 2 * kNB * kTileBytes;
   // The parts of the weighted x: twice for the states alone, where those of the next chunk are made while this one's product
-  // runs.  With the outputs' work once, behind Y, whose buffer of x is then free sooner (N = 64, B=8 T=4096 H=32: 213 us, 261
-  // with two).
+  // runs.  With the outputs' work once, behind Y, whose buffer of x is then free sooner (N = 64, B=8 T=4096 H=32, M in one part: 213 us,
+  // 261 with two).
   static constexpr int kXSets = OUT ? 1 : 2;
   static constexpr int kXS = kC + (OUT ? kNB * kTileBytes : 0), kSH = kXS + kXSets * 3 * kTileBytes;
   static constexpr int kEnd = kSH + (OUT ? 2 * N * 128 : 0);
@@ -59,8 +61,9 @@ struct Smem {
   };
   static constexpr int kBytes = kEnd + int(sizeof(Tail)) + 1024;
 };
-// TMEM columns
-constexpr uint32_t kTG = 0, kTM = 128, kTY1 = 192, kTY2 = 256, kTU = 384;   // kTY2, kTU: two of 64 each
+// TMEM columns.  kTY2: two of 64.  kTU: two of 64 for the states alone; with the outputs one, as XS waits for the state
+// then, and the second part of M behind it.
+constexpr uint32_t kTG = 0, kTM = 128, kTY1 = 192, kTY2 = 256, kTU = 384, kTM2 = 448;
 
 template <int N, bool OUT, bool REV>
 __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p, const __grid_constant__ TileMaps tm, const ChunkOp op) {
@@ -190,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
       if (OUT && i >= 0) {
         if (!(ok = wait.warp(&tl.m_ready[i & 1], ph(i)) && wait.warp(&tl.x_full[i & 1], ph(i)))) break;
         tc::fence_after_sync();
-        if (elected()) {   // Y1(i) = M X (all warps have read Y1(i - 1))
+        if (elected()) {   // Y1(i) = M X, the smaller part of M first (all warps have read Y1(i - 1))
           const uint64_t dx = dX + ((i & 1) * kTileBytes >> 4);
 #pragma unroll 1
-          for (int k = 0; k < kQ / 16; ++k) mma_bf16_ts(tmem + kTY1, tmem + kTM + 8 * k, mn_step(dx, k), kIdY, k > 0);
+          for (int k = 0; k < 2 * (kQ / 16); ++k)
+            mma_bf16_ts(tmem + kTY1, tmem + (k < 8 ? kTM2 : kTM) + 8 * (k & 7), mn_step(dx, k & 7), kIdY, k > 0);
           tc::commit(&tl.y_full[i & 1]);
         }
         __syncwarp();
@@ -209,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         products(tmem + kTY2 + 64 * (e & 1), dC, 32, kTileBytes, NB, dSH, 2048, 8192, 2 * NB, kIdY, &tl.y2_done);
       }
       if (!(ok = wait.warp(&tl.xs_ready[e & 1], ph(e)))) break;       // U(e) = B^T (w X), transposed state [N][64]: three parts
-      products(tmem + kTU + 64 * (e & 1), dBm + bt, 2048, 8192, 2, dXS + (e % SM::kXSets * 3 * kTileBytes >> 4), 2048, 8192, 6, kIdU,
+      products(tmem + kTU + (OUT ? 0 : 64 * (e & 1)), dBm + bt, 2048, 8192, 2, dXS + (e % SM::kXSets * 3 * kTileBytes >> 4), 2048, 8192, 6, kIdU,
                &tl.u_full[e & 1]);
     }
   } else {
@@ -233,8 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
       }
     if (OUT && r > w) {   // the blocks of M behind the diagonal stay zero
       const uint32_t zero[8] = {};
-      st8(lanes + kTM + 16 * r, zero);
-      st8(lanes + kTM + 16 * r + 8, zero);
+#pragma unroll
+      for (int k = 0; k < 16; k += 8) {
+        st8(lanes + kTM + 16 * r + k, zero);
+        st8(lanes + kTM2 + 16 * r + k, zero);
+      }
       tc::wait_st();
     }
     auto put = [&](float* dst, int q0 = 0, int q1 = 16) {   // [64][N]
@@ -336,10 +343,15 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
             if (resets)
 #pragma unroll
               for (int s = 0; s < 16; ++s) v[s] = c + s >= start ? v[s] : 0.f;
-            uint32_t m[8];
+            uint32_t m[8], m2[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m[e] = pack(v[2 * e], v[2 * e + 1]);
+            for (int e = 0; e < 8; ++e) {
+              float2 f = make_float2(v[2 * e], v[2 * e + 1]);
+              m[e] = split(f);
+              m2[e] = pack(f.x, f.y);
+            }
             st8(lanes + kTM + (c >> 1), m);
+            st8(lanes + kTM2 + (c >> 1), m2);
           }
           tc::wait_st();
           tc::fence_before_sync();
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
         if (!(ok = wait.warp(&tl.u_full[i & 1], ph(i)))) break;
         tc::fence_after_sync();
         float u[16];
-        ld16(lanes + kTU + 64 * (i & 1) + 16 * r, u);
+        ld16(lanes + kTU + (OUT ? 0 : 64 * (i & 1)) + 16 * r, u);
         tc::wait_ld();
         tc::fence_before_sync();
 #pragma unroll
