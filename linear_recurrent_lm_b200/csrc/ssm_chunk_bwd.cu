@@ -10,22 +10,26 @@
 //
 // Precision: G and K are products of the bf16 inputs themselves, so W is an fp32 result, and its row and column sums, most
 // of which cancel against each other in the decays' gradient, are taken in fp64 (in fp32 dA was off by 4e-6); S and dS enter the
-// products behind row and far in three bf16 parts (2^-25) and those behind dB and dC in two.  Rounded once to bf16: L o G
-// and L o K off the diagonal, and the scaled dY and X, all of them behind bf16 outputs.
+// products behind row and far in three bf16 parts (2^-26) and those behind dB and dC in two (2^-18), as do L o G and L o K off
+// the diagonal and the scaled dY and X: with one part each, db and dc were off by as much again as their own rounding.
 //
 // One CTA per (b, chunk, group, part of the group's heads); b and c tiles stay in shared memory while it walks the heads,
 // and dB, dC accumulate in TMEM over them.  Sixteen warps work in the same phase (ssm_chunk.cu says why):
 //   A  S into bf16 parts, in_t dy_t          (while G and K are computed)
 //   W  G and K from TMEM: L o G back to TMEM, d L o K to shared memory, the sums
 //   B  d_s out_s x_s, dS into bf16 parts (once the products with S are done)
-//   E  dX
+//   E  dX; the second parts of d L o K and of d_s out_s x_s, each in the place of the first once that has been read (that of
+//      in_t dy_t is in A, in a half of the place of d L o K)
 // while further warps issue MMAs (16), load tiles (17), prepare the decays (18) and, from the sums that the working warps
 // leave, write the per-token scalars of the head before (19).
-// TMEM: [0,128) G, then L o G as bf16 (64) and (L o G)^T dY (64); [128,256) K, then C S^T (64) and B dS^T (64); dB; dC.
+// TMEM: [0,128) G, then both parts of L o G, each 16 columns in the place of theirs, then B dS^T (64); [128,256) K, then C S^T
+// (64) and (L o G)^T dY (64); dB; dC.
 // What bounds it: phase W, by the instructions of one scheduler.  A warp reaches the TMEM lanes of its number modulo four,
 // which is its scheduler too, so the first quadrant's four warps share the eight 16-column units of the longest rows (550
-// instructions each, a third of them fp64): 5000 of about 19000 cycles per chunk and head; the others wait for them.
-// The MMA work is 5600 cycles at N = 128, at the rates measured for these shapes.  B=8 T=4096 H=32 N=128: 684 us.
+// instructions each before the second parts, a third of them fp64): 5000 of about 19000 cycles per chunk and head; the others
+// wait for them.
+// The MMA work is 7100 cycles at N = 128, at the rates measured for these shapes.  B=8 T=4096 H=32 N=128, with the reversed
+// state pass and the sums behind it: 964 us (830 with one part each).
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -35,7 +39,7 @@ namespace {
 using namespace stc;
 
 constexpr int kWorkers = 16, kThreads = 32 * (kWorkers + 4);   // 20 warps of 96 registers; a 21st would leave 80
-constexpr uint32_t kTG = 0, kTM = 0, kTX1 = 64, kTK = 128, kTY2 = 128, kTXi = 192, kTdB = 256, kTdC = 384;
+constexpr uint32_t kTG = 0, kTXi = 0, kTK = 128, kTY2 = 128, kTX1 = 192, kTdB = 256, kTdC = 384;
 
 template <int N>
 struct Smem {
@@ -49,8 +53,8 @@ struct Smem {
     float rp[4][kQ], fp[4][kQ];
     float own_g[kQ], own_k[kQ];
     double sds[kWorkers];
-    unsigned long long bc_full, xy_full, xy_free, gk_full, s_ready, w_ready, y2_full, m_done, ds_ready, xi_full, e_full, ab_free, quad[4],
-        dec_full[3], dec_free[3], sums_free, sc_free, drained;
+    unsigned long long bc_full, xy_full, xy_free, gk_full, s_ready, w_ready, y2_full, m_done, ds_ready, xi_full, xs_done, m2_ready,
+        x2_ready, e_full, ab_free, dec_full[3], dec_free[3], sums_free, sc_free, drained;
     uint32_t tmem;
     int dead;
   };
@@ -99,11 +103,10 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
   if (threadIdx.x == 0) {
     tl.dead = 0;
     unsigned long long* one[] = {&tl.bc_full, &tl.xy_full, &tl.gk_full, &tl.y2_full, &tl.m_done, &tl.xi_full, &tl.e_full,
-                                 &tl.sums_free, &tl.sc_free, &tl.drained};
+                                 &tl.sums_free, &tl.sc_free, &tl.xs_done, &tl.drained};
     for (auto* bar : one) mbar_init(bar, 1);
-    unsigned long long* all[] = {&tl.xy_free, &tl.s_ready, &tl.w_ready, &tl.ds_ready, &tl.ab_free};
+    unsigned long long* all[] = {&tl.xy_free, &tl.s_ready, &tl.w_ready, &tl.ds_ready, &tl.m2_ready, &tl.x2_ready, &tl.ab_free};
     for (auto* bar : all) mbar_init(bar, kWorkers);
-    for (int i = 0; i < 4; ++i) mbar_init(&tl.quad[i], 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(&tl.dec_full[i], 1);
       mbar_init(&tl.dec_free[i], kWorkers + 1);
@@ -232,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       __syncwarp();
       if (!(ok = wait.warp(&tl.s_ready, ph(i)))) break;
       tc::fence_after_sync();
-      if (elected()) {   // dC += (in dY) S, two parts
-        products(tmem + kTdC, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, i > 0);
+      if (elected()) {   // dC += (in dY) S: the second part with the first of S, the first with two of S
+        products(tmem + kTdC, dM1k + (kTileBytes >> 4), 32, 0, 1, dS + (2 * SM::kPart >> 4), 32, 0, 1, kIdN, i > 0);
+        products(tmem + kTdC, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, true);
         tc::commit(&tl.sc_free);
       }
       __syncwarp();
@@ -243,18 +247,33 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         products(tmem + kTY2, dCk, 32, kTileBytes, NB, dS, 2048, 8192, 3 * NB, kIdY, false);   // C S^T, three parts
         tc::commit(&tl.y2_full);
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) mma_bf16_ts(tmem + kTX1, tmem + kTM + 8 * k, mn_step(ddY, k), kIdY, k > 0);   // (L o G)^T dY
+        for (int k = 0; k < 16; ++k)   // (L o G)^T dY, the second part first
+          mma_bf16_ts(tmem + kTX1, tmem + kTG + 16 * (k & 7) + (k < 8 ? 8 : 0), mn_step(ddY, k & 7), kIdY, k > 0);
         products(tmem + kTdB, dM1k, 32, kTileBytes, 2, dCm, 2048, 8192, 2, kIddB, i > 0);      // dB += (L o K d)^T C
         products(tmem + kTdC, dM1m, 2048, 8192, 2, dBm, 2048, 8192, 2, kIddC, true);           // dC += (L o K d) B
         tc::commit(&tl.m_done);
       }
       __syncwarp();
-      if (!(ok = wait.warp(&tl.ds_ready, ph(i)))) break;
+      if (!(ok = wait.warp(&tl.ds_ready, ph(i)) && wait.warp(&tl.m_done, ph(i)))) break;   // (L o G has been read)
       tc::fence_after_sync();
       if (elected()) {
         products(tmem + kTXi, dBk, 32, kTileBytes, NB, dS, 2048, 8192, 3 * NB, kIdY, false);   // B dS^T, three parts
         tc::commit(&tl.xi_full);
         products(tmem + kTdB, dSc, 32, 0, 1, dS + (SM::kPart >> 4), 32, SM::kPart, 2, kIdN, true);   // dB += (d out X) dS, two
+        tc::commit(&tl.xs_done);
+      }
+      __syncwarp();
+      if (!(ok = wait.warp(&tl.m2_ready, ph(i)))) break;
+      tc::fence_after_sync();
+      if (elected()) {   // the second part of L o K d
+        products(tmem + kTdB, dM1k, 32, kTileBytes, 2, dCm, 2048, 8192, 2, kIddB, true);
+        products(tmem + kTdC, dM1m, 2048, 8192, 2, dBm, 2048, 8192, 2, kIddC, true);
+      }
+      __syncwarp();
+      if (!(ok = wait.warp(&tl.x2_ready, ph(i)))) break;
+      tc::fence_after_sync();
+      if (elected()) {   // the second part of d out X, with the first of dS
+        products(tmem + kTdB, dSc, 32, 0, 1, dS + (2 * SM::kPart >> 4), 32, 0, 1, kIdN, true);
         tc::commit(&tl.e_full);
       }
       __syncwarp();
@@ -264,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
     const int w = warp & 3, r = warp >> 2, row = 32 * w + lane;
     const uint32_t lanes = tmem + (uint32_t(32 * w) << 16);
     const int sn = threadIdx.x % N, sp = threadIdx.x / N * PP;   // this thread's state column and first state row
-    WarpBarrier quad{&tl.quad[w], 0};
     bool ok = true;
     // the state (or its gradient) of this thread into three bf16 parts, the smallest first: the tensor core cuts its sums
     // off below their leading bits, which the large part then meets in its own steps only
@@ -291,20 +309,23 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
               make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
       }
     };
-    // this thread's 16 channels of its token row of `tile`, scaled, into the scaled tile
-    auto scaled = [&](int tile, float f) {
+    // this thread's 16 channels of its token row of `tile`, scaled, into the scaled tile (the first part), and the second
+    // part into `second`, if there is one
+    auto scaled = [&](int tile, float f, int second) {
 #pragma unroll 1
       for (int j = 2 * r; j < 2 * r + 2; ++j) {
         const uint32_t o = swz(row, j);
         const uint4 v = *reinterpret_cast<const uint4*>(sm + tile + o);
         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t out[4];
+        uint32_t out[4], rest[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 q = mul2(stc::unpack(in[k]), make_float2(f, f));
-          out[k] = pack(q.x, q.y);
+          float2 q = mul2(stc::unpack(in[k]), make_float2(f, f));
+          out[k] = split(q);
+          rest[k] = pack(q.x, q.y);
         }
         *reinterpret_cast<uint4*>(sm + SM::kSc + o) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (second >= 0) *reinterpret_cast<uint4*>(sm + second + o) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
       }
     };
     auto hand_over = [&](unsigned long long* bar) {
@@ -323,13 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       parts(S);
       if (!(ok = wait.warp(&tl.dec_full[i % 3], unsigned(i / 3) & 1u) && wait.warp(&tl.xy_full, ph(i)))) break;
       const float in = dec.in[row], out = dec.out[row], d = dec.d[row];
-      scaled(SM::kdY, in);
+      scaled(SM::kdY, in, SM::kM1 + kTileBytes);
       hand_over(&tl.s_ready);
       // ---- W: columns t of row s, 16 at a time from the diagonal block on
       if (!(ok = wait.warp(&tl.gk_full, ph(i)) && (i == 0 || wait.warp(&tl.sums_free, ph(i - 1))))) break;
       tc::fence_after_sync();
       double col = 0.0;
-      uint32_t ma[8], mb[8];
+      uint32_t ma[8], mb[8];   // the second parts of d L o K
       {
         const float hi = dec.hi[row], lo = dec.lo[row], fs = decay_between(dec.hi[32 * w + 31], dec.lo[32 * w + 31], hi, lo);
         const bool grow = dec.growing != 0, resets = dec.resets != 0;
@@ -378,21 +399,26 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
               tl.own_k[row] = ok_;
             }
           }
-          uint32_t m[8];
+          uint32_t m[8], gm[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 l2 = make_float2(L[2 * e], L[2 * e + 1]), k2 = make_float2(kv[2 * e], kv[2 * e + 1]);
-            const float2 lg = mul2(l2, make_float2(gv[2 * e], gv[2 * e + 1]));
-            const float2 kd = mul2(mul2(l2, k2), make_float2(d, d)), wd = mul2(lg, k2);
+            float2 lg = mul2(l2, make_float2(gv[2 * e], gv[2 * e + 1]));
+            float2 kd = mul2(mul2(l2, k2), make_float2(d, d));
+            const float2 wd = mul2(lg, k2);
             wv[2 * e] = double(wd.x);
             wv[2 * e + 1] = double(wd.y);
             col += wv[2 * e] + wv[2 * e + 1];
             wv[2 * e] *= double(d);
             wv[2 * e + 1] *= double(d);
-            if (it == 0) ma[e] = pack(lg.x, lg.y);
-            else mb[e] = pack(lg.x, lg.y);
-            m[e] = pack(kd.x, kd.y);
+            gm[e] = split(lg);
+            gm[8 + e] = pack(lg.x, lg.y);
+            m[e] = split(kd);
+            if (it == 0) ma[e] = pack(kd.x, kd.y);
+            else mb[e] = pack(kd.x, kd.y);
           }
+          if (it == 0 && !(ok = wait.warp(&tl.sc_free, ph(i)))) break;   // the second part of in dY has been read
+          st16(lanes + kTG + c0, gm);   // in the place of these columns of G, which no other warp reads
           uint8_t* m1 = sm + SM::kM1 + (c0 >> 6) * kTileBytes;
           *reinterpret_cast<uint4*>(m1 + swz(row, (c0 & 63) >> 3)) = make_uint4(m[0], m[1], m[2], m[3]);
           *reinterpret_cast<uint4*>(m1 + swz(row, ((c0 & 63) >> 3) + 1)) = make_uint4(m[4], m[5], m[6], m[7]);
@@ -400,16 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
           if (lane < 16) tl.rowp[w][c0 + lane] = rs;
         }
       }
+      if (!(ok = ok && wait.warp(&tl.sc_free, ph(i)))) break;
+      if (w == 3) *reinterpret_cast<uint4*>(sm + SM::kM1 + kTileBytes + swz(row, r)) = make_uint4(0, 0, 0, 0);   // it lay there too
       tl.colp[r][row] = col;
-      tc::fence_before_sync();
-      if (!(ok = quad(wait))) break;   // the quadrant's G has been read: L o G takes its place
-      tc::fence_after_sync();
       {
-        const int c0 = 32 * w + 16 * r;
-        if (c0 < kQ) st8(lanes + kTM + (c0 >> 1), ma);
-        if (c0 + 64 < kQ) st8(lanes + kTM + (c0 >> 1) + 32, mb);
-        const uint32_t zero[8] = {};
-        for (int z = 16 * r; z < 32 * w; z += 64) st8(lanes + kTM + (z >> 1), zero);
+        const uint32_t zero[16] = {};
+        for (int z = 16 * r; z < 32 * w; z += 64) st16(lanes + kTG + z, zero);
         tc::wait_st();
       }
       tc::fence_before_sync();
@@ -418,8 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       float S2[PP], dS[PP];   // S again, for <S, dS>: kept since phase A it would be 16 registers through W
       fetch(p.ckpt + (unit * (nc + 1) + c) * 64 * N, S2);
       fetch(p.scratch + sc.dstate + (unit * nc + c) * 64 * N, dS);
-      if (!(ok = wait.warp(&tl.sc_free, ph(i)))) break;
-      scaled(SM::kX, d * out);
+      scaled(SM::kX, d * out, -1);
       if (!(ok = wait.warp(&tl.y2_full, ph(i)))) break;
       tc::fence_after_sync();
       float y2[16];
@@ -455,6 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
       if (!(ok = wait.warp(&tl.m_done, ph(i)))) break;
       __syncwarp();
       if (lane == 0) arrive(&tl.xy_free);
+#pragma unroll
+      for (int it = 0; it < 2; ++it) {   // the second parts of d L o K take the place of the first
+        const int c0 = 32 * w + 16 * (r + 4 * it);
+        const uint32_t(&m)[8] = it == 0 ? ma : mb;
+        if (c0 < kQ) {
+          uint8_t* m1 = sm + SM::kM1 + (c0 >> 6) * kTileBytes;
+          *reinterpret_cast<uint4*>(m1 + swz(row, (c0 & 63) >> 3)) = make_uint4(m[0], m[1], m[2], m[3]);
+          *reinterpret_cast<uint4*>(m1 + swz(row, ((c0 & 63) >> 3) + 1)) = make_uint4(m[4], m[5], m[6], m[7]);
+        }
+      }
+      hand_over(&tl.m2_ready);
       if (!(ok = wait.warp(&tl.xi_full, ph(i)))) break;
       tc::fence_after_sync();
       const int64_t t = t0 + row;
@@ -483,6 +515,19 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
           arrive(&tl.dec_free[i % 3]);
           arrive(&tl.ab_free);
         }
+        if (!(ok = wait.warp(&tl.xs_done, ph(i)))) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {   // the second part of d out X takes the place of the first
+          uint32_t q[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 f = mul2(stc::unpack(xv[4 * j + k]), make_float2(od, od));
+            split(f);
+            q[k] = pack(f.x, f.y);
+          }
+          *reinterpret_cast<uint4*>(sm + SM::kSc + swz(row, 2 * r + j)) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        hand_over(&tl.x2_ready);
         if (t < p.T && range_ok(t, 1, p.T, p.status)) {
           uint4* dx = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dx) + ((b * p.T + t) * p.H + h0 + i) * 64 + 16 * r);
           dx[0] = make_uint4(o[0], o[1], o[2], o[3]);

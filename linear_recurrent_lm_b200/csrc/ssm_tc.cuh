@@ -45,6 +45,13 @@ __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t (&v)[8]) {
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+      "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 
 // One lane of the warp, the same one every time.
 __device__ __forceinline__ bool elected() {
@@ -129,18 +136,6 @@ __device__ __forceinline__ void tma_store_4d(const void* map, const void* src, i
 }
 __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// A barrier of `n` warps that gives up with everyone else: each use toggles the phase.
-struct WarpBarrier {
-  unsigned long long* bar;
-  unsigned phase;
-  __device__ __forceinline__ bool operator()(const Wait& wait) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) arrive(bar);
-    const bool ok = wait.warp(bar, phase);
-    phase ^= 1u;
-    return ok;
-  }
-};
 
 // ---- decays of one chunk.  Lambda_t: sum of log2 decays from the chunk's start up to and with token t, summed in fp64
 // and kept as a pair of floats; r_t: a reset at or before t in the chunk.  Everything is zero behind the row's end.

@@ -19,7 +19,8 @@ pytestmark = pytest.mark.gpu
 
 BOUND = 2.0 ** -14
 CASES = {"plain": dict(B=2, T=300, H=4, G=2, N=64), "wide": dict(B=1, T=391, H=6, G=2, N=128),
-         "long_memory": dict(B=2, T=260, H=3, G=1, N=128, A_scale=1e-2, reset=None), "one_head": dict(B=1, T=900, H=1, G=1, N=64, A_scale=0.1)}
+         "long_memory": dict(B=2, T=260, H=3, G=1, N=128, A_scale=1e-2, reset=None), "one_head": dict(B=1, T=900, H=1, G=1, N=64, A_scale=0.1),
+         "many_heads": dict(B=1, T=200, H=24, G=2, N=128)}
 
 
 def _check(got, ref, size, what):
@@ -41,3 +42,17 @@ def test_outputs_are_rounded_once(W, case):   # noqa: F811
     _, dev, ref = _case(case)
     y, _, _ = W.ssm_forward(**dev, algo="chunked")
     _check(y, S.ssm_forward(**ref)[0], _sizes(ref, True), "y")
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_gradients_are_rounded_once(W, case):   # noqa: F811
+    """dx, ddt, and db, dc, whose sums run over the group's heads as well (more steps, each cut alike)."""
+    rng, dev, ref = _case(case)
+    dy, dy64 = _dev(rng.standard_normal(ref["x"].shape), "bf16")
+    ds, ds64 = _dev(rng.standard_normal(ref["s0"].shape).astype(np.float32))
+    _, _, ws = W.ssm_forward(**dev, algo="chunked")
+    g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo="chunked", **dev)
+    go = S.ssm_backward(dy=dy64, dsT=ds64, **ref)
+    size = _sizes(ref, True, dy64, ds64)
+    for n in ("dx", "ddt", "db", "dc"):
+        _check(g[n], go[n], size[n], n)
