@@ -19,6 +19,9 @@ __device__ __forceinline__ float step_of(const SsmArgs& p, int64_t bt, int64_t h
   return p.softplus ? softplus_of(v) : v;
 }
 
+// A decay exp(d A) that is zero in fp32 (below 2^-150) cuts like a reset: nothing of what is before the token is left.
+__device__ __forceinline__ bool cuts(float d, float A) { return d * A < -103.97208f; }
+
 __host__ __device__ __forceinline__ int64_t chunks_of(int64_t T) { return (T + kSsmChunk - 1) / kSsmChunk; }
 
 // Reverse sums inside segments over the 128 tokens of a chunk held by one warp, 4 consecutive tokens per lane:

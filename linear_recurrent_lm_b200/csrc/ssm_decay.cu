@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmSc
       v[i] = rows[i] - double(d[i]) * cs[i];
       if (CHUNKED) leave += double(d[i]) * double(fr[i]);
       // a decay that is zero cuts like a reset: what is left of its sums is rounding, which a large A would blow up
-      if ((p.reset && p.reset[b * p.T + t0 + i]) || expf(d[i] * A) == 0.f) rst |= 1u << i;
+      if ((p.reset && p.reset[b * p.T + t0 + i]) || cuts(d[i], A)) rst |= 1u << i;
     }
   }
   cut = rst >> 1;   // token i ends its segment where token i + 1 is a reset

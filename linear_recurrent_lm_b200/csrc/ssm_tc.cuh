@@ -138,7 +138,7 @@ __device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.w
 __device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ---- decays of one chunk.  Lambda_t: sum of log2 decays from the chunk's start up to and with token t, summed in fp64
-// and kept as a pair of floats; r_t: a reset at or before t in the chunk.  Everything is zero behind the row's end.
+// and kept as a pair of floats; r_t: a reset (or a decay of zero) at or before t in the chunk.  Everything is zero behind the row's end.
 struct alignas(16) Decays {   // (its rows are read four floats at a time, in arrays of these)
   float hi[kQ], lo[kQ];   // Lambda_t
   float d[kQ];            // step
@@ -193,11 +193,13 @@ __device__ __forceinline__ void chunk_decays(const SsmArgs& p, float A, float bi
   for (int k = 0; k < 4; ++k) {
     const float v = __uint_as_float(unsigned(raw.v[k]) << 16) + bias;
     d[k] = t0 + k < p.T ? (p.softplus ? softplus_of(v) : v) : 0.f;
-    const double x = fmax(double(d[k]) * A2, -1e30);   // nothing is left long before, and sums of 128 stay finite as floats
+    // A step that leaves nothing is a reset and not a term of the sum, which would lose the decays behind it.
+    const bool cut = cuts(d[k], A);
+    const double x = cut ? 0.0 : double(d[k]) * A2;
     grow |= x > 0.0;
     sum += x;
     l[k] = sum;
-    if (raw.rst[k]) last = 4 * lane + k;
+    if (raw.rst[k] || cut) last = 4 * lane + k;
     st[k] = last;
   }
 #pragma unroll

@@ -1,0 +1,53 @@
+"""The selective scan where single tokens, or parameters, leave the ordinary range: a step that clears the state among
+ordinary ones, and what is not a number in a parameter.  Tolerances as in test_gpu_state_space.py."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import state_space as S
+from tests.test_gpu_state_space import FORMS, FP32, W, _close, _close_chunked, _dev, _f64, _sizes, _ssm_case   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,algo", FORMS)
+@pytest.mark.parametrize("step", (60.0, 200.0, 1e4, 6e4, 1e13, 1e18, 1e30))
+def test_one_step_clears_the_state(W, dtype, algo, step):   # noqa: F811
+    """A step of any size at a token with x = 0 decays the state and nothing else: the ordinary decays behind it keep their
+    weights, in every output.  (dx at that token itself is as large as the step, so it is looked at apart.)"""
+    if dtype == "f16" and step > 200:
+        pytest.skip("dx at the token, a few times the step, leaves this type")
+    rng = np.random.default_rng(500)
+    B, T, H, G, N = 2, 300, 4, 2, 64
+    dev, ref = _ssm_case(rng, dtype, B, T, H, G, N, reset=None, A_scale=0.25)
+    big = np.zeros((B, T), bool)
+    big[0, [3, 40, 41, 127, 200]] = True
+    big[1, [0, 128, 255, 299]] = True
+    for b, t in np.argwhere(big):
+        dev["x"][b, t] = 0
+        ref["x"][b, t] = 0
+        dev["dt"][b, t] = step
+    ref["dt"] = _f64(dev["dt"])
+    y, s, ws = W.ssm_forward(**dev, algo=algo)
+    yo, so = S.ssm_forward(**ref)
+    dy, dy64 = _dev(rng.standard_normal(ref["x"].shape), dtype)
+    ds, ds64 = _dev(rng.standard_normal(so.shape).astype(np.float32))
+    g = W.ssm_backward(dy=dy, workspace=ws, dsT=ds, algo=algo, **dev)
+    go = S.ssm_backward(dy=dy64, dsT=ds64, **ref)
+    _close(s, so, "f32", FP32, "s_out")
+    for n in ("dA", "dD", "ddt_bias", "ds0"):
+        _close(g[n], go[n], "f32", FP32, n)
+    got = {"y": y, **g}
+    want = {"y": yo, **go}
+    # dL/da at a token is formed as a difference of sums over the paths of up to 128 tokens (128 terms each, every one rounded
+    # to 2^-53, and none larger than 2^10 of the largest ddt's terms, whose softplus' derivative is at least 2^-10 here): where
+    # a decay leaves next to nothing, ddt is off by up to 128 * 128 * 2^-53 * 2^10 = 2^-29 of that, and not of its own size.
+    size = {"y": np.abs(_sizes(ref, True)), **{n: np.abs(v) for n, v in _sizes(ref, True, dy64, ds64).items()}}
+    size["ddt"] = np.maximum(size["ddt"], 2.0 ** -20 * size["ddt"].max((0, 1)))   # (times 2^-8: 2^-28)
+    for n in ("y", "dx", "ddt", "db", "dc"):
+        for part in (~big, big) if n == "dx" else (np.ones_like(big),):
+            if algo == "chunked":
+                _close_chunked(got[n][part], want[n][part], size[n][part], n)
+            else:
+                _close(got[n][part], want[n][part], dtype, FP32, n)
