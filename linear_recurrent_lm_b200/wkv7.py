@@ -499,6 +499,12 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor)
     return t
 
 
+def _wanted(g: Dict[str, torch.Tensor], name: str, want: bool, shape, dtype, like: torch.Tensor):
+    """An optional gradient in ``g``: made where it is wanted, and what the caller put there is written, so it is checked."""
+    if want or g.get(name) is not None:
+        g[name] = _out(g.get(name), name, shape, dtype, like)
+
+
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -554,12 +560,11 @@ def conv_backward(x, weight, dy, bias=None, s0=None, reset=None, dsT=None, *, si
     d, cv, px, (B, T, D, W) = _conv_args(x, weight, bias, silu, 2, flags)
     g = dict(grads) if grads is not None else {}
     g["dx"] = _out(g.get("dx"), "dx", (B, T, D), x.dtype, x)
-    if want_params:
-        g["dweight"] = _out(g.get("dweight"), "dweight", (D, W), torch.float32, x)
-        g["dbias"] = _out(g.get("dbias"), "dbias", (D,), torch.float32, x)
-    if want_ds0:
-        g["ds0"] = _out(g.get("ds0"), "ds0", (B, W - 1, D), x.dtype, x)
-    tmp = _scratch(lib().wkv7_conv_scratch_bytes(d, cv), x) if want_params else None
+    _wanted(g, "dweight", want_params, (D, W), torch.float32, x)
+    _wanted(g, "dbias", want_params, (D,), torch.float32, x)
+    _wanted(g, "ds0", want_ds0, (B, W - 1, D), x.dtype, x)
+    params = g.get("dweight") is not None or g.get("dbias") is not None
+    tmp = _scratch(lib().wkv7_conv_scratch_bytes(d, cv), x) if params else None
     st = lib().wkv7_conv_backward(d, cv, px, _dense(s0, "s0", (B, W - 1, D), x.dtype, x), _mask(reset, "reset", (B, T), x),
                                   _dense(dy, "dy", (B, T, D), x.dtype, x), _dense(dsT, "dsT", (B, W - 1, D), x.dtype, x),
                                   g["dx"].data_ptr(), _addr(g.get("dweight")), _addr(g.get("dbias")), _addr(g.get("ds0")),
@@ -633,10 +638,8 @@ def ssm_backward(x, dt, A, b, c, dy, workspace, D=None, dt_bias=None, s0=None, r
     for n, shape in shapes.items():
         g[n] = _out(g.get(n), n, shape, x.dtype, x)
     for n, on in (("dA", True), ("dD", D is not None), ("ddt_bias", dt_bias is not None)):
-        if on:
-            g[n] = _out(g.get(n), n, (H,), torch.float32, x)
-    if want_ds0:
-        g["ds0"] = _out(g.get("ds0"), "ds0", (B, H, N_HEAD, N), torch.float32, x)
+        _wanted(g, n, on, (H,), torch.float32, x)
+    _wanted(g, "ds0", want_ds0, (B, H, N_HEAD, N), torch.float32, x)
     need = 4 * B * H * (-(-T // 128) + 1) * N_HEAD * N if T else 0   # the states alone, whichever form wrote them
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"the backward needs the forward's workspace of at least {need} bytes")
@@ -711,11 +714,9 @@ def rms_backward(x, weight, dout, eps: float, *, gate=None, dh=None, groups: int
     g = dict(grads) if grads is not None else {}
     px = _dense(x, "x", x.shape, x.dtype, x)
     g["dx"] = _out(g.get("dx"), "dx", x.shape, x.dtype, x)
-    if gate is not None:
-        g["dgate"] = _out(g.get("dgate"), "dgate", x.shape, x.dtype, x)
-    if want_params:
-        g["dweight"] = _out(g.get("dweight"), "dweight", (x.shape[-1],), torch.float32, x)
-    tmp = _scratch(lib().wkv7_rms_scratch_bytes(d, rn), x) if want_params else None
+    _wanted(g, "dgate", gate is not None, x.shape, x.dtype, x)
+    _wanted(g, "dweight", want_params, (x.shape[-1],), torch.float32, x)
+    tmp = _scratch(lib().wkv7_rms_scratch_bytes(d, rn), x) if g.get("dweight") is not None else None
     st = lib().wkv7_rms_backward(d, rn, px, _dense(gate, "gate", x.shape, x.dtype, x),
                                  _dense(dout, "dout", x.shape, x.dtype, x), _dense(dh, "dh", x.shape, x.dtype, x),
                                  g["dx"].data_ptr(), _addr(g.get("dgate")), _addr(g.get("dweight")), _addr(tmp), _now(x))

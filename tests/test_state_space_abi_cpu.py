@@ -161,3 +161,21 @@ def test_valid_calls_need_a_gpu(L):
     assert _ssm(L, _desc(L), _ssm_struct(L)) == L.ERR_CUDA
     assert _conv(L, _desc(L), L.Conv(16, 4, 1, FAKE, None, 0)) == L.ERR_CUDA
     assert L.lib().wkv7_rms_forward(_desc(L), L.Rms(256, 1, FAKE, 1e-5, 0, 0), FAKE, None, None, FAKE, None, None) == L.ERR_CUDA
+
+
+def test_binding_checks_every_gradient_it_is_given(L):
+    """An entry of ``grads`` is written whether or not it was asked for, so a wrong one is refused either way.  (The functions
+    under their device check, with host tensors: they refuse before they reach the library.)"""
+    import torch
+    z = torch.zeros
+    x, w = z(2, 8, 16), z(16, 4)
+    for bad, name in ((z(2, 3, 8), "ds0"), (z(16, 2), "dweight"), (z(16, dtype=torch.float64), "dbias"), (z(2, 8, 8), "dx")):
+        with pytest.raises(ValueError, match=name):
+            L.conv_backward.__wrapped__(x, w, x, grads={name: bad}, want_params=False, want_ds0=False)
+    xs, bc, A, ws = z(1, 8, 2, 64), z(1, 8, 1, 64), z(2), z(1 << 18, dtype=torch.uint8)
+    for bad, name in ((z(1, 2, 64, 32), "ds0"), (z(1), "dD"), (z(3), "ddt_bias"), (z(2, dtype=torch.float64), "dA"), (z(1, 8, 1, 32), "db")):
+        with pytest.raises(ValueError, match=name):
+            L.ssm_backward.__wrapped__(xs, z(1, 8, 2), A, bc, bc, xs, ws, grads={name: bad}, want_ds0=False)
+    for bad, name in ((z(8), "dweight"), (z(2, 8, 8), "dgate")):
+        with pytest.raises(ValueError, match=name):
+            L.rms_backward.__wrapped__(x, z(16), x, 1e-5, grads={name: bad}, want_params=False)
