@@ -51,3 +51,31 @@ def test_one_step_clears_the_state(W, dtype, algo, step):   # noqa: F811
                 _close_chunked(got[n][part], want[n][part], size[n][part], n)
             else:
                 _close(got[n][part], want[n][part], dtype, FP32, n)
+
+
+@pytest.mark.parametrize("dtype,algo", FORMS)
+@pytest.mark.parametrize("name", ("A", "dt_bias", "D"))
+def test_what_is_not_a_number_in_a_parameter_shows(W, dtype, algo, name):   # noqa: F811
+    """A NaN in one head's parameter reaches that head's outputs and gradients, and no other head's (db and dc are the group's)."""
+    import torch
+    rng = np.random.default_rng(510)
+    dev, _ = _ssm_case(rng, dtype, 2, 150, 4, 4, 64, reset=None)
+    dy = torch.randn(2, 150, 4, 64, device="cuda").to(dev["x"].dtype)
+
+    def run():
+        y, s, ws = W.ssm_forward(**dev, algo=algo)
+        return {"y": y, "s": s, **W.ssm_backward(dy=dy, workspace=ws, algo=algo, **dev)}
+    want = run()
+    dev[name] = dev[name].clone()
+    dev[name][1] = float("nan")
+    got = run()
+    other = [0, 2, 3]
+    dims = {"y": 2, "s": 1, "dx": 2, "ddt": 2, "db": 2, "dc": 2, "ds0": 1, "dA": 0, "dD": 0, "ddt_bias": 0}
+    for n, t in got.items():
+        a, b = t.movedim(dims[n], 0), want[n].movedim(dims[n], 0)
+        assert torch.equal(a[other], b[other]), n
+    reached = {"A": ("y", "s", "dA", "ddt_bias"), "dt_bias": ("y", "s", "dA", "ddt_bias"), "D": ("y", "dx")}[name]
+    for n in reached:
+        assert got[n].movedim(dims[n], 0)[1].isnan().any(), n
+    if name == "A":
+        assert got["y"][:, 1:, 1].isnan().all() and got["s"][:, 1].isnan().all()
