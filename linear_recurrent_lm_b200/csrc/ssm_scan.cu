@@ -46,7 +46,9 @@ struct ScanOp {
   // The walk may be cut into `segments` runs of `per` tokens: a first pass (LOCAL) leaves each run's end state from
   // zero and its total decay, and the second starts every run from what those before it left.
   int64_t segments, per;
-  void *seg_state, *seg_decay;           // [B,H,segments] states [R][K] and decays, fp32 (transposed scans: fp64)
+  void* seg_state;                       // [B,H,segments] states [R][K], fp32 (transposed scans: fp64)
+  double* seg_decay;                     // [B,H,segments] decays: of a run's many tokens they may leave fp32's range where
+                                         // what they multiply brings the product back
 };
 
 // 16 bytes of staged values.
@@ -108,19 +110,29 @@ __global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, co
       }
   if (!LOCAL)
     for (int64_t j = unit * op.segments; j < unit * op.segments + seg; ++j) {
-      const F f = static_cast<const F*>(op.seg_decay)[j];
+      const double f = op.seg_decay[j];
       const F* z = static_cast<const F*>(op.seg_state) + j * (R * K);
+      auto join = [&](auto g) {   // Z = g Z + z
 #pragma unroll
-      for (int i = 0; i < kRows; ++i)
+        for (int i = 0; i < kRows; ++i)
 #pragma unroll
-        for (int u = 0; u < NI; ++u)
+          for (int u = 0; u < NI; ++u)
 #pragma unroll
-          for (int e = 0; e < EV; ++e) {
-            F& v = Z[i][EV * u + e];
-            v = (f == F(0) ? F(0) : f * v) + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
-          }
+            for (int e = 0; e < EV; ++e) {
+              F& v = Z[i][EV * u + e];
+              v = F(g * v) + z[(r0 + i) * K + (8 * u + lane8) * EV + e];
+            }
+      };
+      if (f == 0.0) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int e = 0; e < NI * EV; ++e) Z[i][e] = F(0);
+      }
+      if (f < 1e37 && (f > 1e-37 || f == 0.0)) join(F(f));
+      else join(f);   // (f16 B=3 T=777 H=6 forward: 36 us, 39 with this throughout)
     }
-  F total = 1;
+  double total = 1.0;
   auto put_state = [&](auto* dst, F f) {
     using D = std::remove_pointer_t<decltype(dst)>;
     using D2 = typename std::conditional<sizeof(D) == 8, double2, float2>::type;
@@ -281,7 +293,7 @@ __global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, co
   }
   if (LOCAL) {
     put_state(static_cast<F*>(op.seg_state) + blockIdx.x * int64_t(R * K), F(1));
-    if (tid == 0) static_cast<F*>(op.seg_decay)[blockIdx.x] = total;
+    if (tid == 0) op.seg_decay[blockIdx.x] = total;
   } else if (seg == op.segments - 1) {
     if (op.last) {
       F f = 1;
@@ -324,7 +336,7 @@ void cut(const SsmArgs& p, ScanOp* op, float* seg) {
   op->per = (p.T + k - 1) / k;
   op->segments = op->per > 0 ? (p.T + op->per - 1) / op->per : 1;
   op->seg_state = seg;
-  op->seg_decay = reinterpret_cast<F*>(seg) + units * op->segments * R * K;
+  op->seg_decay = reinterpret_cast<double*>(reinterpret_cast<F*>(seg) + units * op->segments * R * K);
 }
 
 template <typename T, int N>
@@ -493,10 +505,11 @@ cudaError_t run_dtype(const SsmArgs& p, int dtype, bool backward, cudaStream_t s
 
 }  // namespace
 
-// fp32 elements of the runs' states and decays (fp64: twice as many); whole 16 bytes, as several follow one another.
+// fp32 elements of the runs' states and (fp64) decays, enough for twice as much where the states are fp64 too; whole 16
+// bytes, as several follow one another.
 int64_t ssm_run_floats(int64_t B, int64_t T, int64_t H, int N) {
   const int64_t k = scan_segments(B * H, T);
-  return k > 1 ? (B * H * k * (kHeadP * N + 1) + 3) / 4 * 4 : 0;
+  return k > 1 ? (B * H * k * (kHeadP * N + 2) + 3) / 4 * 4 : 0;
 }
 
 cudaError_t launch_ssm_scan_fwd(const SsmArgs& p, int dtype, cudaStream_t s) { return run_dtype(p, dtype, false, s); }

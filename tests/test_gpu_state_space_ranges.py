@@ -79,3 +79,30 @@ def test_what_is_not_a_number_in_a_parameter_shows(W, dtype, algo, name):   # no
         assert got[n].movedim(dims[n], 0)[1].isnan().any(), n
     if name == "A":
         assert got["y"][:, 1:, 1].isnan().all() and got["s"][:, 1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16", "f16"))
+def test_runs_whose_decay_leaves_the_range(W, dtype):   # noqa: F811
+    """Token order, a row cut into runs, decays of e^3 per token: over a run of 35 the product is e^105, no fp32 number, but what
+    it multiplies is zero until the last tokens (and, for the gradients, behind the first)."""
+    import torch
+    rng = np.random.default_rng(520)
+    B, T, H, N = 1, 140, 2, 64
+    dev, ref = _ssm_case(rng, dtype, B, T, H, 1, N, reset=None, state=False, params=False, strided=False)
+    assert W.lib().wkv7_ssm_workspace_bytes(W.make_desc(B, T, H, dev["x"].dtype, "scan", N=N), W.Ssm(1, None, None, None, 0, 0, 0, 0, 0)) \
+        > 4 * B * H * 3 * 64 * N                                    # the row is cut into runs
+    dev["dt"].fill_(1.0)
+    dev["A"].fill_(3.0)
+    ref["dt"], ref["A"] = np.ones((B, T, H)), np.full(H, 3.0)
+    dev["x"][:, : T - 2] = 0
+    ref["x"] = _f64(dev["x"])
+    y, s, ws = W.ssm_forward(**dev, softplus=False, algo="scan")
+    yo, so = S.ssm_forward(**ref, softplus=False)
+    _close(s, so, "f32", FP32, "s_out")
+    _close(y, yo, dtype, FP32, "y")
+    dy = torch.zeros_like(dev["x"])
+    dy[:, :2] = torch.randn(B, 2, H, 64, device="cuda").to(dy.dtype)
+    g = W.ssm_backward(dy=dy, workspace=ws, softplus=False, algo="scan", **dev)
+    go = S.ssm_backward(dy=_f64(dy), softplus=False, **ref)
+    for n in ("ds0", "dx", "db", "dc", "ddt", "dA"):
+        _close(g[n], go[n], "f32" if n in ("ds0", "dA") else dtype, FP32, n)
