@@ -52,3 +52,46 @@ def test_cut_rows_remember(W, monkeypatch, dtype, algo, reset, H, T, N):   # noq
         step = np.logaddexp(0.0, ref["dt"] + ref["dt_bias"])
         assert np.exp((step * ref["A"]).sum(1)).min() > 0.05
     _ssm_check(W, rng, dtype, algo, dev, ref)
+
+
+# ------------------------------------------------------------------ convolution
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("taps,T,run,state", ((4, 1203, 64, True), (3, 1203, 64, False), (2, 1200, 64, True), (4, 1201, 64, False), (4, 603, 32, True),
+                                              (3, 301, 16, True)))
+def test_conv_long_runs(W, dtype, taps, T, run, state):   # noqa: F811
+    """Enough rows and channels for runs of 64, 32 and 16 tokens (the backward's; the forward's are half as long): several batches of
+    four in a run, with resets inside, at the ends and just behind the ends of batches and runs, and a ragged last run."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(700 + T + taps)
+    B, D = 8, 2048
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
+    x, dy = r(B, T, D + 8).to(_t(dtype))[..., 8:], r(B, T, D).to(_t(dtype))
+    w, bias = r(D, taps), r(D)
+    s0, dsT = (r(B, taps - 1, D).to(_t(dtype)) for _ in range(2)) if state else (None, None)
+    desc = W.make_desc(B, T, 0, _t(dtype))
+    assert W.lib().wkv7_conv_scratch_bytes(desc, W.Conv(D, taps, 1, None, None, 0)) == 4 * B * -(-T // run) * (taps + 1) * D
+    reset = (torch.rand(B, T, generator=g, device="cuda") < 0.01).to(torch.uint8)
+    reset[1] = 0                                           # a row without any
+    for t in (3, 4, 5, 31, 32, 63, 64, 65, 67, 127, 130, 200, 201, T - 1):
+        reset[t % B, t] = 1
+    y, s_out = W.conv_forward(x, w, bias, s0, reset)
+    got = W.conv_backward(x, w, dy, bias, s0, reset, dsT)
+    # the formulas in fp64: the taps that no reset cuts off
+    x64, w64, b64 = (v.double().requires_grad_(True) for v in (x, w, bias))
+    past = (torch.zeros(B, taps - 1, D, device="cuda", dtype=torch.float64) if s0 is None else s0.double()).requires_grad_(True)
+    full = torch.cat([past, x64], 1)
+    seg = torch.cat([torch.zeros(B, taps - 1, device="cuda", dtype=torch.int64), reset.long().cumsum(1)], 1)
+    u = b64 + 0.0 * x64
+    for j in range(taps):
+        at = taps - 1 - j
+        u = u + full[:, at:at + T] * w64[:, taps - 1 - j] * (seg[:, at:at + T] == seg[:, taps - 1:]).double()[..., None]
+    y64 = torch.nn.functional.silu(u)
+    s64 = full[:, T:] * (seg[:, T:] == seg[:, -1:]).double()[..., None]
+    _close64(y, y64.detach(), dtype, "y")
+    assert torch.equal(s_out.double(), s64.detach())
+    loss = (y64 * dy.double()).sum() + ((s64 * dsT.double()).sum() if state else 0.0)
+    loss.backward()
+    _close64(got["dx"], x64.grad, dtype, "dx")
+    _close64(got["ds0"], past.grad, dtype, "ds0")
+    _close64(got["dweight"], w64.grad, "f32", "dweight")
+    _close64(got["dbias"], b64.grad, "f32", "dbias")
