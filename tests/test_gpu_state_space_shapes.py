@@ -95,3 +95,61 @@ def test_conv_long_runs(W, dtype, taps, T, run, state):   # noqa: F811
     _close64(got["ds0"], past.grad, dtype, "ds0")
     _close64(got["dweight"], w64.grad, "f32", "dweight")
     _close64(got["dbias"], b64.grad, "f32", "dbias")
+
+
+# ------------------------------------------------------------------ norm
+# rows, channels, slices per row: more slices than the forward has CTAs (2368) and more rows than one wave of the backward's,
+# with one, two and four vectors per thread, several slices per CTA, and a ragged end
+NORMS = ((5003, 2048, 1), (100003, 64, 1), (2501, 12288, 1), (2500, 16384, 1), (2503, 6144, 3), (20011, 192, 3))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("kind", ("residual", "gate"))
+@pytest.mark.parametrize("rows,D,groups", NORMS)
+def test_rms_many_rows(W, dtype, kind, rows, D, groups):   # noqa: F811
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(800 + D)
+    x, z, dout, dh = (torch.randn(rows, D, generator=g, device="cuda").to(_t(dtype)) for _ in range(4))
+    w = 1.0 + 0.2 * torch.randn(D, generator=g, device="cuda")
+    f = W.rms_forward(x, w, 1e-5, groups=groups, **{kind: z})
+    if kind == "residual":
+        assert torch.equal(f["h"], (x.float() + z.float()).to(x.dtype))
+        got = W.rms_backward(f["h"], w, dout, 1e-5, groups=groups, dh=dh)
+        h = f["h"].double()
+    else:
+        got = W.rms_backward(x, w, dout, 1e-5, groups=groups, gate=z)
+        s = torch.sigmoid(z.double())
+        h = x.double() * z.double() * s
+    v = h.view(rows, groups, -1)
+    rstd = (v.square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    xh = (v * rstd).view(rows, D)
+    _close64(f["out"], xh * w.double(), dtype, "out")
+    d64 = dout.double()
+    _close64(got["dweight"], (d64 * xh).sum(0), "f32", "dweight")
+    q = (d64 * w.double()).view_as(v)
+    dv = (rstd * (q - xh.view_as(v) * (q * xh.view_as(v)).mean(-1, keepdim=True))).view(rows, D)
+    if kind == "residual":
+        _close64(got["dx"], dv + dh.double(), dtype, "dx")
+    else:
+        _close64(got["dx"], dv * z.double() * s, dtype, "dx")
+        _close64(got["dgate"], dv * x.double() * s * (1.0 + z.double() * (1.0 - s)), dtype, "dgate")
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("block,rows,D,groups", ((128, 5003, 2048, 1), (-1, 5003, 2048, 1), (128, 40009, 128, 1), (-1, 100003, 64, 1), (128, 2501, 12288, 1),
+                                                 (-1, 2501, 16384, 1), (128, 5003, 768, 2), (-1, 20011, 192, 3)))
+def test_rms_e4m3_many_rows(W, dtype, block, rows, D, groups):   # noqa: F811
+    """Half a step of e4m3 per code (2^-4 of the value, 2^-10 of the scale below its normal range) and the scale's largest value
+    over 448, for every slice, with the sum stored beside it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(900 + D)
+    x, r = (torch.randn(rows, D, generator=g, device="cuda").to(_t(dtype)) for _ in range(2))
+    w = 1.0 + 0.2 * torch.randn(D, generator=g, device="cuda")
+    f = W.rms_forward(x, w, 1e-5, residual=r, groups=groups, quant_block=block)
+    assert torch.equal(f["h"], (x.float() + r.float()).to(x.dtype))
+    v = f["h"].double().view(rows, groups, -1)
+    ref = ((v * (v.square().mean(-1, keepdim=True) + 1e-5).rsqrt()).view(rows, D) * w.double()).view(rows, -1, 128 if block > 0 else D // groups)
+    scale = f["scale"].double().view(rows, -1, 1)
+    assert ((scale - ref.abs().amax(2, keepdim=True) / 448.0).abs() <= 1e-5 * scale).all()
+    code = f["q"].float().double().view_as(ref) * scale
+    assert ((code - ref).abs() <= torch.maximum(ref.abs() * 2.0 ** -4, scale * 2.0 ** -10) * (1.0 + 1e-4)).all()
