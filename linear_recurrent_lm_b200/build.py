@@ -37,7 +37,8 @@ def _stale(target: str, deps) -> bool:
 VARIANTS = {
     # name: (library, object folder, extra nvcc flags)
     "release": (LIB, OBJ, []),
-    # every kernel index checked against its buffer; a failed check sets a status bit (WKV7_ERR_BOUNDS)
+    # kernel indices checked against their buffers; a failed check sets a status bit (WKV7_ERR_BOUNDS).  Left out: masks and
+    # parameters of one value per head or channel, and the shared-memory tiles of the chunked selective scan
     "debug": (LIB_DEBUG, OBJ + "_debug", ["-DWKV7_DEBUG"]),
 }
 

@@ -93,6 +93,9 @@ __global__ void __launch_bounds__(kRunThreads, kFwdMinCtas<T>) conv_fwd_kernel(c
   const T* x = static_cast<const T*>(p.x) + b * p.T * p.x_ld + d0;
   T* y = static_cast<T*>(p.y) + b * p.T * p.D + d0;
   const uint8_t* reset = p.reset ? p.reset + b * p.T : nullptr;
+  auto load = [&](int64_t t) {
+    return rows_ok((b * p.T + t) * p.x_ld + d0, V, p.B * p.T, p.x_ld, p.D, p.status) ? VT::load(x + t * p.x_ld) : typename VT::R{};
+  };
   auto token = [&](const typename VT::R& raw, int64_t t) {   // u_t from its input and the window, which moves on
     float v[V], u[V];
     VT::get(raw, v);
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kRunThreads, kFwdMinCtas<T>) conv_fwd_kernel(c
   typename VT::R next[kBatch];   // loads run one batch ahead
   if (t + kBatch <= t1)
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) next[i] = VT::load(x + (t + i) * p.x_ld);
+    for (int i = 0; i < kBatch; ++i) next[i] = load(t + i);
   for (; t + kBatch <= t1; t += kBatch) {
     typename VT::R raw[kBatch];
     unsigned cut = 0;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kRunThreads, kFwdMinCtas<T>) conv_fwd_kernel(c
     for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
     if (t + 2 * kBatch <= t1)
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) next[i] = VT::load(x + (t + kBatch + i) * p.x_ld);
+      for (int i = 0; i < kBatch; ++i) next[i] = load(t + kBatch + i);
     if (reset)
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) cut |= reset[t + i] ? 1u << i : 0u;
@@ -150,12 +153,14 @@ __global__ void __launch_bounds__(kRunThreads, kFwdMinCtas<T>) conv_fwd_kernel(c
       for (int j = 0; j < W - 1; ++j)
 #pragma unroll
         for (int e = 0; e < V; ++e) win[j][e] = 0.f;
-    token(VT::load(x + t * p.x_ld), t);
+    token(load(t), t);
   }
   if (p.s_out && t1 == p.T)
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j)   // slot W-2-j holds x_{T-1-j}
-      VT::store(static_cast<T*>(p.s_out) + (b * (W - 1) + (W - 2 - j)) * p.D + d0, win[j]);
+    for (int j = 0; j < W - 1; ++j) {   // slot W-2-j holds x_{T-1-j}
+      const int64_t off = (b * (W - 1) + (W - 2 - j)) * p.D + d0;
+      if (range_ok(off, V, p.B * (W - 1) * p.D, p.status)) VT::store(static_cast<T*>(p.s_out) + off, win[j]);
+    }
 }
 
 // Backward: with du_t = dy_t silu'(u_t) (u recomputed), dx_t = sum_j w[j] du_{t+j} over the taps that no reset
@@ -183,6 +188,10 @@ __global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p,
   const T* dy = static_cast<const T*>(p.dy) + b * p.T * p.D + d0;
   const uint8_t* reset = p.reset ? p.reset + b * p.T : nullptr;
   T* dx = static_cast<T*>(p.dx) + b * p.T * p.D + d0;
+  auto load = [&](int64_t t, typename VT::R& rx, typename VT::R& rg) {
+    if (rows_ok((b * p.T + t) * p.x_ld + d0, V, p.B * p.T, p.x_ld, p.D, p.status)) rx = VT::load(x + t * p.x_ld);
+    if (range_ok((b * p.T + t) * p.D + d0, V, p.B * p.T * p.D, p.status)) rg = VT::load(dy + t * p.D);
+  };
   // One token: the gradient of u_t, which goes to the filter and to the inputs behind its taps; then the input that is
   // W - 1 tokens back is complete.  PLAIN: a token of this run, all of whose taps count, and that input is of this run too.
   auto token = [&](const typename VT::R& rx, const typename VT::R& rg, int64_t t, auto plain) {
@@ -231,22 +240,23 @@ __global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p,
     }
     if (td < t0 && !(t0 == 0 && td < 0)) return;
     if (p.dsT && td >= p.T - (W - 1) && p.T - 1 - td <= age) {   // it is in s_out, not cut off
-      float s[V];
-      VT::get(VT::load(static_cast<const T*>(p.dsT) + (b * (W - 1) + td - (p.T - (W - 1))) * p.D + d0), s);
+      float s[V] = {};
+      const int64_t off = (b * (W - 1) + td - (p.T - (W - 1))) * p.D + d0;
+      if (range_ok(off, V, p.B * (W - 1) * p.D, p.status)) VT::get(VT::load(static_cast<const T*>(p.dsT) + off), s);
 #pragma unroll
       for (int e = 0; e < V; ++e) dxp[W - 1][e] += s[e];
     }
     if (td >= 0) {
       if (range_ok((b * p.T + td) * p.D + d0, V, p.B * p.T * p.D, p.status)) VT::store(dx + td * p.D, dxp[W - 1]);
     } else if (p.ds0) {
-      VT::store(static_cast<T*>(p.ds0) + (b * (W - 1) + W - 1 + td) * p.D + d0, dxp[W - 1]);
+      const int64_t off = (b * (W - 1) + W - 1 + td) * p.D + d0;
+      if (range_ok(off, V, p.B * (W - 1) * p.D, p.status)) VT::store(static_cast<T*>(p.ds0) + off, dxp[W - 1]);
     }
   };
   auto slow = [&](int64_t t) {   // any token, also behind the run or the row
     typename VT::R rx{}, rg{};
     if (t < p.T) {
-      rx = VT::load(x + t * p.x_ld);
-      rg = VT::load(dy + t * p.D);
+      load(t, rx, rg);
       if (reset && reset[t]) {
         age = 0;
 #pragma unroll
@@ -268,10 +278,7 @@ __global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p,
   auto ahead = [&](int64_t t) {
     if (t + kBatch <= plain_end)
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        nx[i] = VT::load(x + (t + i) * p.x_ld);
-        ng[i] = VT::load(dy + (t + i) * p.D);
-      }
+      for (int i = 0; i < kBatch; ++i) load(t + i, nx[i], ng[i]);
   };
   ahead(t);
 #pragma unroll 1
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kRunThreads) conv_bwd_kernel(const ConvArgs p,
   }
 #pragma unroll 1
   for (; t < tend; ++t) slow(t);
-  if (p.scratch) {   // [run][W + 1][D]: dw of weight[.][0..W-1], then dbias
+  if (p.scratch && range_ok(br * (W + 1) * p.D + d0, W * p.D + V, p.B * runs * (W + 1) * p.D, p.status)) {   // [run][W + 1][D]: dw of weight[.][0..W-1], then dbias
     float* o = p.scratch + br * (W + 1) * p.D + d0;
 #pragma unroll
     for (int j = 0; j < W; ++j)
@@ -326,6 +333,9 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs p) {
   const int64_t id = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t b = id / nv, d0 = (id - b * nv) * V;
   if (b >= p.B) return;
+  if (!range_ok(b * p.D + d0, V, p.B * p.D, p.status) || !rows_ok(b * p.x_ld + d0, V, p.B, p.x_ld, p.D, p.status) ||
+      !range_ok((b * (W - 1) + W - 2) * p.D + d0, V, p.B * (W - 1) * p.D, p.status))
+    return;
   T* y = static_cast<T*>(p.y) + b * p.D + d0;
   if (p.active && !p.active[b]) {
     const float zero[V] = {};

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
 #pragma unroll
             for (int e = 0; e < V; e += 2) two(q, e) = mul2(two(h[i], e), both(inv));
             store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + v * V, q);
-            if ((lane & (128 / V - 1)) == 0) p.scale[(base + v * V) >> 7] = sc;
+            if ((lane & (128 / V - 1)) == 0 && range_ok((base + v * V) >> 7, 1, total >> 7, p.status)) p.scale[(base + v * V) >> 7] = sc;
           }
         }
         top = max_nan(top, m);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kMaxThreads<T, VPT>) rms_fwd_kernel(const RmsA
           for (int e = 0; e < V; e += 2) two(q, e) = mul2(two(h[i], e), both(inv));
           store_e4m3<T, V>(static_cast<uint8_t*>(p.out) + base + (i * s.tps + lane) * V, q);
         }
-      if (lane == 0 && slice < s.slices) p.scale[slice] = sc;
+      if (lane == 0 && slice < s.slices && range_ok(slice, 1, p.rows * p.groups, p.status)) p.scale[slice] = sc;
     }
   }
 }
@@ -300,7 +300,7 @@ rms_bwd_kernel(const RmsArgs p, const Shape s, int64_t nb) {
         if (GATE) VT::store(static_cast<T*>(p.dother) + o, dz);
       }
   }
-  if (!p.scratch) return;
+  if (!p.scratch || !range_ok(blk * p.D + g * s.L, s.L, nb * p.D, p.status)) return;
   float* out = p.scratch + blk * p.D + g * s.L;
   if (s.spc == 1) {
 #pragma unroll

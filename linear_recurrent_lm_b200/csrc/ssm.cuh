@@ -13,7 +13,7 @@ __device__ __forceinline__ float softplus_of(float v) { return log1pf(expf(-fabs
 // The step d_t of token row `bt` (= b T + t) for head h, and (optionally) its argument.
 template <typename T>
 __device__ __forceinline__ float step_of(const SsmArgs& p, int64_t bt, int64_t h, float* raw = nullptr) {
-  float v = Elt<T>::to_f32(static_cast<const T*>(p.dt)[bt * p.dt_ld + h]);
+  float v = rows_ok(bt * p.dt_ld + h, 1, p.B * p.T, p.dt_ld, p.H, p.status) ? Elt<T>::to_f32(static_cast<const T*>(p.dt)[bt * p.dt_ld + h]) : 0.f;
   if (p.dt_bias) v += __ldg(p.dt_bias + h);
   if (raw) *raw = v;
   return p.softplus ? softplus_of(v) : v;

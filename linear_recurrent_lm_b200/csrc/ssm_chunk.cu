@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
       for (int i = 0; i < n; ++i) {
         ok = false;
         const int t0 = int(chunk(i) * kQ), s = i & 1;
+        if (!in_bounds(t0 >= 0 && t0 < p.T && b < p.B && g < p.G, p.status)) break;
         if (i >= 2 && !wait(&tl.u_full[s], ph(i - 2))) break;
         mbar_arrive_expect_tx(&tl.b_full[s], NB * kTileBytes);
         for (int j = 0; j < NB; ++j)
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
       tc::wait_st();
     }
     auto put = [&](float* dst, int q0 = 0, int q1 = 16) {   // [64][N]
-      if (mine)
+      if (mine && range_ok(at, 15 * N + 1, 64 * N, p.status))
 #pragma unroll
         for (int q = 0; q < 16; ++q)
           if (q >= q0 && q < q1) dst[at + q * N] = S[q];
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
     // The state that enters chunk e, four of a thread's sixteen rows at a time: its stores are spread over the phases, as
     // they would fill the store queue at once (256 of 128 bytes per CTA).
     auto put_part = [&](int e, int k) {
-      if (op.states) put(op.states + (unit * op.stride + chunk(e)) * 64 * N, 4 * k, 4 * k + 4);
+      if (op.states && range_ok(chunk(e), 1, op.stride, p.status)) put(op.states + (unit * op.stride + chunk(e)) * 64 * N, 4 * k, 4 * k + 4);
     };
     // The weighted x of chunk e in three bf16 parts (its buffer has been read).  The smallest part first: the tensor core
     // cuts its sums off below their leading bits, which the large part then meets in its own eight steps only.
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_kernel(const SsmArgs p,
           __syncwarp();
           if (lane == 0) arrive(&tl.sh_ready[e & 1]);
           put_part(e, 0);
-        } else if (op.states) {
+        } else if (op.states && range_ok(chunk(e), 1, op.stride, p.status)) {
           put(op.states + (unit * op.stride + chunk(e)) * 64 * N);
         }
       }

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
 
   if (warp == 17) {
     // ------------------------------------------------------------ loads
-    if (lane == 0 && n > 0) {
+    if (lane == 0 && n > 0 && in_bounds(t0 < p.T && b < p.B && h0 + n <= p.H, p.status)) {
       mbar_arrive_expect_tx(&tl.bc_full, 2 * NB * kTileBytes);
       for (int j = 0; j < NB; ++j) {
         tma_load_4d(sm + SM::kB + j * kTileBytes, &tm.b, 64 * j, int(g), t0, int(b), &tl.bc_full);
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) ssm_chunk_bwd_kernel(const SsmArg
         arrive(&tl.sums_free);
       }
       const int64_t o = unit * nc * kQ + t0 + lane;
+      if (!range_ok(o - lane, kQ, p.B * p.H * nc * kQ, p.status)) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         reinterpret_cast<double*>(p.scratch + sc.row)[o + 32 * q] = row[q];

@@ -27,6 +27,8 @@ __global__ void __launch_bounds__(256) decay_kernel(const SsmArgs p, const SsmSc
   const int64_t unit = w / nc, c = w - unit * nc, b = unit / p.H, h = unit - b * p.H;
   const float A = __ldg(p.A + h);
   const int64_t t0 = c * kSsmChunk + 4 * lane, o = unit * tp + t0;
+  const bool in = range_ok(o, 4, p.B * p.H * tp, p.status) && (t0 >= p.T || range_ok((b * p.T + t0) * p.H + h, 1, p.B * p.T * p.H, p.status));
+  if (kDebugChecks && !__all_sync(0xffffffffu, in)) return;
   const double *rows = reinterpret_cast<const double*>(p.scratch + sc.row) + o, *cols = reinterpret_cast<const double*>(p.scratch + sc.col) + o;
   const float4 own = *reinterpret_cast<const float4*>(p.scratch + sc.own + o);
   const float4 xd = *reinterpret_cast<const float4*>(p.scratch + sc.xdy + o);

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, co
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
         const int row = r0 + i, col = (8 * u + lane8) * EV + e;   // init is [64][N]: transposed where R = N
-        Z[i][EV * u + e] = !LOCAL && op.init ? F(__ldg(op.init + unit * R * K + (TR ? col * R + row : row * K + col))) : F(0);
+        const int64_t at = unit * R * K + (TR ? col * R + row : row * K + col);
+        Z[i][EV * u + e] = !LOCAL && op.init && range_ok(at, 1, p.B * p.H * R * K, p.status) ? F(__ldg(op.init + at)) : F(0);
       }
   if (!LOCAL)
     for (int64_t j = unit * op.segments; j < unit * op.segments + seg; ++j) {
@@ -166,7 +167,9 @@ __global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, co
           const void* base = which == 0 ? op.rin : which == 1 ? op.kin : op.con;
           const int64_t ld = which == 0 ? op.rin_ld : which == 1 ? op.kin_ld : op.con_ld;
           const bool grp = which == 0 ? op.rin_g : which == 1 ? op.kin_g : op.con_g;
-          raw[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(base) + bt * ld + (grp ? g : h) * width + j * V));
+          const int64_t off = bt * ld + (grp ? g : h) * width + j * V;
+          if (rows_ok(off, V, p.B * T_, ld, (grp ? p.G : p.H) * width, p.status))
+            raw[q] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(base) + off));
         }
       }
     }
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(8 * R / kRows) scan_kernel(const SsmArgs p, co
       const F f = s_fio[buf][i][0], in = s_fio[buf][i][1];
       if (mark >> i & 1u) {
         const int64_t t = token(pos0 + i);
-        if (!LOCAL && op.chunk_state && stores(t))
+        if (!LOCAL && op.chunk_state && stores(t) && range_ok(t / kSsmChunk, 1, op.chunk_stride, p.status))
           put_state(static_cast<F*>(op.chunk_state) + (unit * op.chunk_stride + t / kSsmChunk) * (R * K), REV ? f : F(1));
         if (f == F(0))
 #pragma unroll
@@ -371,6 +374,11 @@ __global__ void __launch_bounds__(256) heads_kernel(const SsmArgs p, const SsmSc
   if (w >= total) return;
   const int64_t bt = w / p.G, g = w - bt * p.G, b = bt / p.T, t = bt - b * p.T, hg = p.H / p.G;
   const int64_t tp = chunks_of(p.T) * kSsmChunk;
+  if (!rows_ok(bt * p.b_ld + g * N, N, p.B * p.T, p.b_ld, p.G * N, p.status) ||
+      !rows_ok(bt * p.c_ld + g * N, N, p.B * p.T, p.c_ld, p.G * N, p.status) ||
+      !rows_ok(bt * p.x_ld + g * hg * kHeadP, hg * kHeadP, p.B * p.T, p.x_ld, p.H * kHeadP, p.status) ||
+      !range_ok((bt * p.H + g * hg) * N, hg * N, p.B * p.T * p.H * N, p.status) || !range_ok(w * N, N, total * N, p.status))
+    return;
   float bv[E], cv[E], db[E] = {}, dc[E] = {}, bc = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {

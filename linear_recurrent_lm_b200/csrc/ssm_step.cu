@@ -23,7 +23,10 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(const SsmArgs p) 
   const int64_t units = p.B * p.H, hg = p.H / p.G;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t b = unit / p.H, h = unit - b * p.H, g = h / hg;
-    if (!range_ok((unit * kHeadP + i) * N, N, units * kHeadP * N, p.status)) continue;
+    if (!range_ok((unit * kHeadP + i) * N, N, units * kHeadP * N, p.status) ||
+        !rows_ok(b * p.x_ld + h * kHeadP + i, 1, p.B, p.x_ld, p.H * kHeadP, p.status) ||
+        !rows_ok(b * p.b_ld + g * N, N, p.B, p.b_ld, p.G * N, p.status) || !rows_ok(b * p.c_ld + g * N, N, p.B, p.c_ld, p.G * N, p.status))
+      continue;
     T* y = static_cast<T*>(p.y) + unit * kHeadP;
     if (p.active && !p.active[b]) {
       if (q == 0) y[i] = Elt<T>::from_f32(0.f);

@@ -167,7 +167,7 @@ struct RawSteps {
     const int64_t t0 = c * kQ + 4 * (threadIdx.x & 31), bt = b * p.T + t0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const bool ok = t0 + k < p.T;
+      const bool ok = t0 + k < p.T && rows_ok((bt + k) * p.dt_ld + h, 1, p.B * p.T, p.dt_ld, p.H, p.status);
       v[k] = ok ? static_cast<const unsigned short*>(p.dt)[(bt + k) * p.dt_ld + h] : 0;
       rst[k] = ok && p.reset ? p.reset[bt + k] : 0;
     }
