@@ -555,14 +555,16 @@ wkv7_status_t wkv7_ssm_forward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, co
 
 /*
  * Reverse mode, from the workspace that the forward of the same arguments
- * wrote (the algo may differ: only the states are read): dy [B,T,H,64], dsT [B,H,64,N] fp32 (gradient of
- * s_out, or NULL) give dx [B,T,H,64], ddt [B,T,H], db, dc [B,T,G,N] (desc->dtype; db and dc
- * are summed over the group's heads), dA [H], dD [H], ddt_bias [H] fp32 (each
- * may be NULL) and ds0 [B,H,64,N] fp32 (or NULL).  All are written, not added
- * to.  ddt is the gradient of the dt input (before the bias and softplus).
- * `scratch` holds wkv7_ssm_scratch_bytes(desc, sp) bytes
- * (WKV7_ERR_WORKSPACE if it or the workspace is NULL when T > 0).  ds0 must
- * not be dsT (WKV7_ERR_UNSUPPORTED).
+ * wrote (the algo may differ: CHUNKED reads the states alone, and SCAN, which
+ * walks forward again, nothing, so that NULL will do there): dy [B,T,H,64],
+ * dsT [B,H,64,N] fp32 (gradient of s_out, or NULL) give dx [B,T,H,64], ddt
+ * [B,T,H], db, dc [B,T,G,N] (desc->dtype; db and dc are summed over the
+ * group's heads), dA [H], dD [H], ddt_bias [H] fp32 (each may be NULL) and ds0
+ * [B,H,64,N] fp32 (or NULL).  All are written, not added to.  ddt is the
+ * gradient of the dt input (before the bias and softplus).  `scratch` holds
+ * wkv7_ssm_scratch_bytes(desc, sp) bytes (WKV7_ERR_WORKSPACE if it, or under
+ * CHUNKED the workspace, is NULL when T > 0).  ds0 must not be dsT
+ * (WKV7_ERR_UNSUPPORTED).
  */
 size_t wkv7_ssm_scratch_bytes(const wkv7_desc_t* desc, const wkv7_ssm_t* sp);
 wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const void* x, const void* dt,

@@ -275,7 +275,7 @@ wkv7_status_t wkv7_ssm_backward(const wkv7_desc_t* d, const wkv7_ssm_t* sp, cons
   TRY(check_ptrs(n > 0, {x, b, c, dy, dx, ddt, db, dc}));
   TRY(check_ptrs(n > 0, {dt}, elt(d)));
   TRY(check_ptrs(false, {s0, dsT, ds0, workspace, scratch, dA, dD, ddt_bias}));
-  if (n > 0 && (!workspace || !scratch)) return WKV7_ERR_WORKSPACE;
+  if (n > 0 && (!scratch || (!workspace && chunked(d, false)))) return WKV7_ERR_WORKSPACE;   // token order walks from s0 again
   if (n > 0 && ds0 && ds0 == dsT) return WKV7_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) {   // no tokens: the parameters have no gradient, the state's passes through

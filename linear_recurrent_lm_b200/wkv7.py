@@ -631,7 +631,8 @@ def ssm_backward(x, dt, A, b, c, dy, workspace, D=None, dt_bias=None, s0=None, r
                  softplus: bool = True, grads=None, want_ds0: bool = True, algo: str = "auto",
                  flags: int = 0) -> Dict[str, torch.Tensor]:
     """Reverse mode of ``ssm_forward`` from its workspace, dy [B,T,H,64] and dsT (gradient of s_out, or None): dict of
-    dx, ddt, db, dc, fp32 dA, dD, ddt_bias (the last two where D and dt_bias are given) and, where wanted, ds0."""
+    dx, ddt, db, dc, fp32 dA, dD, ddt_bias (the last two where D and dt_bias are given) and, where wanted, ds0.  Token order
+    ("scan", which "auto" is for fp32 and fp16) reads no workspace: None will do."""
     d, sp, ptrs, (B, T, H, G, N) = _ssm_args(x, dt, A, b, c, D, dt_bias, softplus, 2, algo, flags)
     g = dict(grads) if grads is not None else {}
     shapes = {"dx": (B, T, H, N_HEAD), "ddt": (B, T, H), "db": (B, T, G, N), "dc": (B, T, G, N)}
@@ -641,13 +642,14 @@ def ssm_backward(x, dt, A, b, c, dy, workspace, D=None, dt_bias=None, s0=None, r
         _wanted(g, n, on, (H,), torch.float32, x)
     _wanted(g, "ds0", want_ds0, (B, H, N_HEAD, N), torch.float32, x)
     need = 4 * B * H * (-(-T // 128) + 1) * N_HEAD * N if T else 0   # the states alone, whichever form wrote them
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
+    reads = x.dtype == torch.bfloat16 and algo != "scan"   # token order walks forward again
+    if reads if workspace is None else workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"the backward needs the forward's workspace of at least {need} bytes")
     tmp = _scratch(lib().wkv7_ssm_scratch_bytes(d, sp), x)
     st = lib().wkv7_ssm_backward(d, sp, *ptrs, _dense(s0, "s0", (B, H, N_HEAD, N), torch.float32, x),
                                  _mask(reset, "reset", (B, T), x), _dense(dy, "dy", (B, T, H, N_HEAD), x.dtype, x),
                                  _dense(dsT, "dsT", (B, H, N_HEAD, N), torch.float32, x),
-                                 _dense(workspace, "workspace", workspace.shape, workspace.dtype, x),
+                                 None if workspace is None else _dense(workspace, "workspace", workspace.shape, workspace.dtype, x),
                                  *(_addr(g.get(n)) for n in ("dx", "ddt", "db", "dc", "dA", "dD", "ddt_bias", "ds0")),
                                  tmp.data_ptr(), _now(x))
     _check(st, "wkv7_ssm_backward")

@@ -106,3 +106,20 @@ def test_runs_whose_decay_leaves_the_range(W, dtype):   # noqa: F811
     go = S.ssm_backward(dy=_f64(dy), softplus=False, **ref)
     for n in ("ds0", "dx", "db", "dc", "ddt", "dA"):
         _close(g[n], go[n], "f32" if n in ("ds0", "dA") else dtype, FP32, n)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16", "f16"))
+def test_token_order_backward_without_a_workspace(W, dtype):   # noqa: F811
+    """Token order walks forward again: no workspace and the same bits; the chunked form refuses."""
+    import torch
+    rng = np.random.default_rng(530)
+    dev, _ = _ssm_case(rng, dtype, 2, 200, 4, 2, 64)
+    dy = torch.randn(2, 200, 4, 64, device="cuda").to(dev["x"].dtype)
+    _, _, ws = W.ssm_forward(**dev, algo="scan")
+    want = W.ssm_backward(dy=dy, workspace=ws, algo="scan", **dev)
+    got = W.ssm_backward(dy=dy, workspace=None, algo="scan", **dev)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    if dtype == "bf16":
+        for algo in ("auto", "chunked"):
+            with pytest.raises(ValueError, match="workspace"):
+                W.ssm_backward(dy=dy, workspace=None, algo=algo, **dev)

@@ -179,3 +179,16 @@ def test_binding_checks_every_gradient_it_is_given(L):
     for bad, name in ((z(8), "dweight"), (z(2, 8, 8), "dgate")):
         with pytest.raises(ValueError, match=name):
             L.rms_backward.__wrapped__(x, z(16), x, 1e-5, grads={name: bad}, want_params=False)
+
+
+def test_workspace_of_the_backward(L):
+    """CHUNKED (AUTO for bf16, whatever the length) refuses a missing workspace; token order, which reads none, does not."""
+    import torch
+    sp = _ssm_struct(L)
+    back = lambda **k: L.lib().wkv7_ssm_backward(_desc(L, **k), sp, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, None, FAKE, FAKE, FAKE, FAKE,   # noqa: E731
+                                                 None, None, None, None, FAKE, None)
+    for k in (dict(), dict(T=4), dict(algo="chunked")):
+        assert back(**k) == L.ERR_WORKSPACE, k
+    if not torch.cuda.is_available():      # (these pass the checks, and would be launched)
+        for k in (dict(algo="scan"), dict(dtype="float32"), dict(dtype="float16")):
+            assert back(**k) == L.ERR_CUDA, k
