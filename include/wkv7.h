@@ -444,8 +444,13 @@ wkv7_status_t wkv7_state_compose(const wkv7_desc_t* desc, const float* S, const 
  * are 0 or WKV7_FLAG_CHECK_FINITE (the same scan of the floating outputs).
  * Errors as for wkv7_forward; algo is ignored except by wkv7_ssm_forward and
  * wkv7_ssm_backward.  Sums, states, decays and statistics are fp32 (running
- * sums of log decays fp64).  Parameter gradients are summed in a fixed order:
- * repeated calls give the same bits.
+ * sums of log decays fp64).  What is rounded to fewer bits on the way: the
+ * operands of CHUNKED's products, split into bf16 parts, three (2^-26 of a
+ * term) for states, parameter gradients and ddt and two (2^-18) for y, dx, db
+ * and dc, so that every output is off by its own rounding and fp32 arithmetic;
+ * and SiLU's sigmoid of 16-bit types (2^-21, and |v| 2^-23 for negative v).
+ * Parameter gradients are summed in a fixed order: repeated calls give the
+ * same bits.
  *
  * Token strides: an input whose struct has a `*_ld` field may be a slice of a
  * wider row-major tensor (the convolution's output holds x, b and c side by
@@ -537,7 +542,10 @@ wkv7_status_t wkv7_conv_step(const wkv7_desc_t* desc, const wkv7_conv_t* cv, con
  * it under SCAN, and nothing across a reset.  CHUNKED multiplies whole chunks
  * with masked weights of zero, so there it may reach every output of its
  * 128-token chunk, earlier tokens included, and the states and chunks after
- * it: fill padding with finite values.
+ * it: fill padding with finite values.  The same comes of decays above one
+ * (d_t A[h] > 0) whose product over tokens of one chunk passes 2^127, and of a
+ * d_t whose product with c . b does; SCAN takes both.  A decay that is zero in
+ * fp32 cuts like a reset under either.
  */
 typedef struct {
   int64_t G;            /* groups: heads that share b and c are consecutive; H % G == 0 */
@@ -589,7 +597,9 @@ wkv7_status_t wkv7_ssm_step(const wkv7_desc_t* desc, const wkv7_ssm_t* sp, const
  *       = x * silu(other)                      (gate != 0)
  *   out = h / sqrt(mean(h^2 over the slice) + eps) * weight
  * The norm is of the sum as it is stored (rounded to desc->dtype), which is
- * what the backward reads.
+ * what the backward reads.  The mean of squares is fp32: a slice whose root
+ * mean square is above 1e18 passes its range (out is then 0), and below
+ * 1e-18 it counts as zero beside eps.  NaN and infinity reach their slice.
  *
  *   desc     B, T, dtype (H and N ignored)
  *   rn       D channels; D % groups == 0, D / groups a multiple of 8 and at
