@@ -55,11 +55,6 @@ __device__ __forceinline__ bool range_ok(int64_t off, int64_t n, int64_t total, 
   return in_bounds(off >= 0 && n >= 0 && off + n <= total, status);
 }
 
-// The same in `rows` rows of `width` elements whose starts are `ld` apart.
-__device__ __forceinline__ bool rows_ok(int64_t off, int64_t n, int64_t rows, int64_t ld, int64_t width, int* status) {
-  return range_ok(off, n, (rows - 1) * ld + width, status);
-}
-
 // Wall-clock limit of one bounded wait on a staging barrier (the copies it waits for take microseconds).
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 

@@ -2,8 +2,14 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace wkv7 {
+
+// Debug build: elements [off, off + n) inside `rows` rows of `width` elements whose starts are `ld` apart.
+__device__ __forceinline__ bool rows_ok(int64_t off, int64_t n, int64_t rows, int64_t ld, int64_t width, int* status) {
+  return range_ok(off, n, (rows - 1) * ld + width, status);
+}
 
 // sigmoid(v), from which silu(v) = v sigmoid(v).  The 16-bit types use the hardware's exponential and reciprocal, five
 // instructions instead of a dozen; fp32 uses the accurate ones.  Relative error: 2^-21 of the two, and for negative v up to
