@@ -10,7 +10,10 @@
 // read.  Up to 32 threads reduce by shuffles alone; wider slices add one pass through shared memory.  Short
 // slices share a CTA of 128 threads; CTAs are that small so that several independent ones per SM cover each other's
 // reductions.  Measured for bf16, 67 M elements, slices of 2048: forward with residual 86 us (6.2 TB/s), plain 55 us (4.9),
-// backward 85 us (4.7); slices of 64 48 us; slices of 8192 3.8 to 4.8 TB/s, of 16384 3.2 to 4.2.
+// backward 85 us (4.7); slices of 64 48 us; the same bytes in fp32: 83, 47, 77 and 46 us.  Wide slices are slower: of 8192 plain,
+// with residual and backward 3.9, 5.7 and 4.4 TB/s (fp32 5.6, 6.1, 3.2), of 16384 3.3, 5.2 and 3.6 (fp32 4.3, 5.2, 2.9).  One of
+// 16384 bf16 takes 512 threads with four vectors each and 92 (backward 126) registers: an SM holds one such CTA, which loads,
+// reduces and stores with nothing else under way (a quarter of the warps, issue slots 32 and 50 % busy); of 8192 it holds two.
 #include <cuda_fp8.h>
 
 #include "kernels.h"

@@ -28,8 +28,8 @@
 // separate warps (M, state, XS) therefore ran at 7300 to 11600 cycles per chunk; all warps in the same phase, loops rolled,
 // share the fetches: about 6500.  MMA work per chunk and head at N = 128, in cycles at the rates measured for these shapes
 // (a product of 64 columns with A in shared memory is bound by reading it): G 512, C S^T 784, M X 520, state 1176.
-// B=8 T=4096 H=32 N=128: 240 us (219 with M in one part; 256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed
-// state pass 140 us.
+// B=8 T=4096 H=32 N=128: 238 us (219 with M in one part; 256 rows of heads on 148 SMs: 1.73 rounds cost two), the reversed
+// state pass 137 us.
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 
@@ -45,8 +45,8 @@ struct Smem {
   static constexpr int kNB = N / 64;             // 64-column tiles of b and c
   static constexpr int kX = 0, kB = kX + 2 * kTileBytes, kC = kB + 2 * kNB * kTileBytes;
   // The parts of the weighted x: twice for the states alone, where those of the next chunk are made while this one's product
-  // runs.  With the outputs' work once, behind Y, whose buffer of x is then free sooner (N = 64, B=8 T=4096 H=32, M in one part: 213 us,
-  // 261 with two).
+  // runs.  With the outputs' work once, behind Y, whose buffer of x is then free sooner (N = 64, B=8 T=4096 H=32, measured with M in
+  // one part: 213 us, 261 with two).
   static constexpr int kXSets = OUT ? 1 : 2;
   static constexpr int kXS = kC + (OUT ? kNB * kTileBytes : 0), kSH = kXS + kXSets * 3 * kTileBytes;
   static constexpr int kEnd = kSH + (OUT ? 2 * N * 128 : 0);

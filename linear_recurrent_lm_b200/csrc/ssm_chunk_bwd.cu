@@ -28,8 +28,9 @@
 // which is its scheduler too, so the first quadrant's four warps share the eight 16-column units of the longest rows (550
 // instructions each before the second parts, a third of them fp64): 5000 of about 19000 cycles per chunk and head; the others
 // wait for them.
-// The MMA work is 7100 cycles at N = 128, at the rates measured for these shapes.  B=8 T=4096 H=32 N=128, with the reversed
-// state pass and the sums behind it: 964 us (830 with one part each).
+// The MMA work is 7100 cycles at N = 128, at the rates measured for these shapes.  B=8 T=4096 H=32 N=128: 808 us, and with the
+// reversed state pass and the sums behind it 960 (830 with one part each: nearly all of the difference is W's instructions, as
+// the second products run beside them).
 #include "ssm_chunk.h"
 #include "ssm_tc.cuh"
 

@@ -12,7 +12,9 @@
 // same numbers are added here and cancel exactly.
 //   dL/dd_t = A dL/da_t + col_t + own_t,   own_t = (x . dy)(b . c);   ddt = dL/dd sigmoid(dt + bias)
 //
-// One warp per (b, h, chunk), 4 tokens per lane; latency-bound (a few microseconds), 16 bytes read per token-head.
+// One warp per (b, h, chunk), 4 tokens per lane.  Per token and head it reads the sums (8 + 8 + 4 + 4 bytes, 4 more where
+// `far` is apart) and dt, and writes ddt: 34 bytes in all for bf16 CHUNKED, 36 MB and 24 us for B=8 T=4096 H=32, as the tokens of
+// dt and ddt are H elements apart; the sums per head after it, one warp each, 8 us.
 #include "ssm.cuh"
 
 namespace wkv7 {
